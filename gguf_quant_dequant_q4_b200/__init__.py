@@ -49,6 +49,11 @@ SIGNATURES = {
     "kq_gather_mix": (_int, [_vp, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _vp, _vp]),
     "kq_moe_glu_gather": (_int, [_int, _vp, _vp, _i32, _i64, _i64, _vp, _vp, _i64, _i32, _i32, ctypes.c_float,
                                  _vp, _vp, _vp]),
+    "kq_kv_plan": (_int, [_vp, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp]),
+    "kq_kv_append": (_int, [_int, _vp, _vp, _int, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _i64, _i32, _vp, _vp]),
+    "kq_kv_attention_workspace": (_int, [_i32, _i32, _i32, _i32, ctypes.POINTER(_i64)]),
+    "kq_kv_attention": (_int, [_int, _vp, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _i64, _i32, _vp,
+                               _i64, ctypes.c_float, _i32, _i32, _vp, _vp, _i64, _vp, _vp]),
 }
 ACT_SILU, ACT_GELU_TANH, ACT_SILU_LIMIT = 0, 1, 2
 
@@ -342,4 +347,164 @@ def moe_glu_gather(x: torch.Tensor, gate_bank: torch.Tensor, up_bank: torch.Tens
     _need_cuda(x, gate_bank, up_bank, ids, out, err)
     _check(lib().kq_moe_glu_gather(qtype, _ptr(gate_bank), _ptr(up_bank), e, n, k, _ptr(x), _ptr(ids), t, top_k,
                                    act, limit, _ptr(out), _ptr(err), _stream(stream)), "kq_moe_glu_gather")
+    return out
+
+
+# --------------------------------------------------- KV cache in q4_0 pages
+# A pool is uint8 [n_pages, n_kv_heads, page_size, row_bytes(Q4_0, head_dim)],
+# one for keys and one for values; a slot is page * page_size + offset.
+
+
+def _same_device(*ts) -> torch.device:
+    dev = {t.device for t in ts if t is not None}
+    if len(dev) != 1:
+        raise ValueError(f"all tensors must be on one device, got {sorted(map(str, dev))}")
+    return dev.pop()
+
+
+def _call(dev: torch.device, stream, what: str, *args) -> None:
+    """The library call ``what`` on ``dev`` and that device's current stream (or ``stream``)."""
+    f = getattr(lib(), what)
+    if dev.index == torch.cuda.current_device():
+        _check(f(*args, _stream(stream)), what)
+    else:
+        with torch.cuda.device(dev):
+            _check(f(*args, _stream(stream)), what)
+
+
+def _scratch(dev: torch.device, stream, *shape, dtype=torch.int32) -> torch.Tensor:
+    """Memory of the stream that the call runs on (the caching allocator gives
+    freed memory to later work of the stream it was allocated on only)."""
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, dtype=dtype, device=dev)
+
+
+def _need_pool(pool: torch.Tensor, what: str, qtype: int, heads: int, dim: int) -> None:
+    _need(pool, what, 1)
+    if pool.dim() != 4 or pool.shape[1] != heads:
+        raise ValueError(f"{what}: [pages, {heads}, page_size, row_bytes] expected, got {tuple(pool.shape)}")
+    if _whole_blocks(qtype, dim) and pool.shape[3] != row_bytes(qtype, dim):
+        raise ValueError(f"{what}: rows of {row_bytes(qtype, dim)} bytes expected for head_dim = {dim}, got {pool.shape[3]}")
+
+
+def _token_rows(x: torch.Tensor, what: str) -> int:
+    """Elements between the tokens of x [tokens, heads, head_dim], whose heads
+    and values are packed (a slice of a fused product's columns is such a view)."""
+    if x.dim() != 3:
+        raise ValueError(f"{what}: [tokens, heads, head_dim] expected, got {tuple(x.shape)}")
+    t, h, d = x.shape
+    if (d > 1 and x.stride(2) != 1) or (h > 1 and x.stride(1) != d):
+        raise ValueError(f"{what}: heads and values of a token must be contiguous")
+    return x.stride(0) if t > 1 else h * d
+
+
+def kv_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+            taken: torch.Tensor, page_size: int, cap: int, taken_out: torch.Tensor | None = None,
+            err: torch.Tensor | None = None, stream=None):
+    """Plan of a step from the requests' lengths (all int32, on the device):
+    (seq_lens [B], cu_new [B + 1], slot_map [cap], positions [cap]).  Takes the
+    pages that the new tokens need from free_pages (from place taken[0] on),
+    writes them into block_table [B, max_blocks] and the new count to taken_out
+    (default: taken itself).  Slots and positions behind the last token are -1.
+    What does not fit gets slot -1 and sets DEV_TOO_MANY in err."""
+    n = cached_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError(f"block_table: [{n}, max_blocks] expected, got {tuple(block_table.shape)}")
+    if taken_out is None:
+        taken_out = taken
+    for t, what, count in ((cached_lens, "cached_lens", n), (new_lens, "new_lens", n), (block_table, "block_table", None),
+                           (free_pages, "free_pages", None), (taken, "taken", 1), (taken_out, "taken_out", 1), (err, "err", 1)):
+        _need(t, what, 4, count)
+    _need_cuda(cached_lens, new_lens, block_table, free_pages, taken, taken_out, err)
+    dev = _same_device(cached_lens, new_lens, block_table, free_pages, taken, taken_out, err)
+    cap = int(cap)
+    if cap < 0:
+        raise ValueError(f"cap must not be negative, got {cap}")
+    seq, cu, first, slots, pos = _scratch(dev, stream, 3 * n + 1 + 2 * cap).split([n, n + 1, n, cap, cap])
+    _call(dev, stream, "kq_kv_plan", _ptr(cached_lens), _ptr(new_lens), n, page_size, _ptr(block_table),
+          block_table.shape[1], _ptr(free_pages), free_pages.numel(), _ptr(taken), _ptr(taken_out), _ptr(seq), _ptr(cu),
+          _ptr(first), _ptr(slots), _ptr(pos), cap, _ptr(err))
+    return seq, cu, slots, pos
+
+
+_F32, _BF16 = 0, 30  # ggml type ids of plain values
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, qtype: int,
+              slot_map: torch.Tensor, err: torch.Tensor | None = None, stream=None) -> None:
+    """Encode k, v [tokens, kv_heads, head_dim] (float32 or bfloat16; views of a
+    fused product's columns are fine) into the pools' slots; slot -1: left out."""
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError(f"k and v must have one shape and type, got {tuple(k.shape)} {k.dtype}, {tuple(v.shape)} {v.dtype}")
+    if k.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("keys and values must be float32 or bfloat16")
+    ks, vs = _token_rows(k, "k"), _token_rows(v, "v")
+    t, h, d = k.shape
+    _need_pool(k_pool, "k_pool", qtype, h, d)
+    _need_pool(v_pool, "v_pool", qtype, h, d)
+    if k_pool.shape != v_pool.shape:
+        raise ValueError(f"v_pool: shape {tuple(k_pool.shape)} expected, got {tuple(v_pool.shape)}")
+    _need(slot_map, "slot_map", 4, t)
+    _need(err, "err", 4, 1)
+    _need_cuda(k_pool, v_pool, slot_map, err)
+    if not (k.is_cuda and v.is_cuda):
+        raise ValueError("all tensors must be CUDA tensors")
+    dev = _same_device(k, v, k_pool, v_pool, slot_map, err)
+    _call(dev, stream, "kq_kv_append", qtype, _ptr(k), _ptr(v), _F32 if k.dtype == torch.float32 else _BF16, t, ks, vs, h, d,
+          _ptr(slot_map), _ptr(k_pool), _ptr(v_pool), k_pool.shape[0], k_pool.shape[2], _ptr(err))
+
+
+def kv_attention_workspace(n_heads: int, n_kv_heads: int, head_dim: int, max_new: int) -> int:
+    """Bytes of work space that kv_attention needs on the current device."""
+    b = _i64()
+    _check(lib().kq_kv_attention_workspace(n_heads, n_kv_heads, head_dim, max_new, ctypes.byref(b)),
+           "kq_kv_attention_workspace")
+    return b.value
+
+
+def kv_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, qtype: int, block_table: torch.Tensor,
+                 seq_lens: torch.Tensor, cu_new: torch.Tensor, max_new: int, scale: float | None = None,
+                 causal: bool = True, window: int = 0, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, err: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of the new tokens q [tokens, heads, head_dim] (bfloat16) over the
+    cached keys and values of their sequences, bfloat16 of q's shape.  seq_lens,
+    cu_new as kv_plan gives them; max_new: the largest number of new tokens of a
+    sequence; scale defaults to head_dim ** -0.5; window 0: no window.  A token
+    that sees no key gets zeros; rows of no sequence are left as they are."""
+    q = _bf16_bits(q)
+    qs = _token_rows(q, "q")
+    t, hq, d = q.shape
+    h = k_pool.shape[1] if k_pool.dim() == 4 else 0
+    _need_pool(k_pool, "k_pool", qtype, h, d)
+    _need_pool(v_pool, "v_pool", qtype, h, d)
+    if k_pool.shape != v_pool.shape:
+        raise ValueError(f"v_pool: shape {tuple(k_pool.shape)} expected, got {tuple(v_pool.shape)}")
+    n = seq_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError(f"block_table: [{n}, max_blocks] expected, got {tuple(block_table.shape)}")
+    _need(block_table, "block_table", 4)
+    _need(seq_lens, "seq_lens", 4)
+    _need(cu_new, "cu_new", 4, n + 1)
+    _need(err, "err", 4, 1)
+    if out is not None:
+        _need(out, "out", 2, t * hq * d)
+    if not q.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors")
+    _need_cuda(k_pool, v_pool, block_table, seq_lens, cu_new, out, workspace, err)
+    dev = _same_device(q, k_pool, v_pool, block_table, seq_lens, cu_new, out, workspace, err)
+    if out is None:
+        out = torch.empty(t, hq, d, dtype=q.dtype, device=dev)
+    if workspace is None:
+        if dev.index == torch.cuda.current_device():
+            need = kv_attention_workspace(hq, h, d, max_new)
+        else:
+            with torch.cuda.device(dev):
+                need = kv_attention_workspace(hq, h, d, max_new)
+        workspace = _scratch(dev, stream, need, dtype=torch.uint8)
+    _call(dev, stream, "kq_kv_attention", qtype, _ptr(q), t, qs, hq, h, d, _ptr(cu_new), _ptr(seq_lens), n, int(max_new),
+          _ptr(k_pool), _ptr(v_pool), k_pool.shape[0], k_pool.shape[2], _ptr(block_table), block_table.shape[1],
+          d ** -0.5 if scale is None else scale, int(bool(causal)), int(window), _ptr(out), _ptr(workspace),
+          workspace.numel() * workspace.element_size(), _ptr(err))
     return out

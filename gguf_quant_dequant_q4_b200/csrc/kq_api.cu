@@ -53,6 +53,36 @@ int check_weights(int type, const void* w, int64_t n, int64_t k) {
     if (n > 0 && !aligned16(w)) return KQ_ERR_ALIGNMENT;
     return KQ_OK;
 }
+
+// Limits of the KV-cache calls: tokens, table places and free pages are
+// counted in 32 bits with room for sums of two.
+constexpr int64_t kMaxKvTokens = int64_t(1) << 30;
+
+// A block table row of max_blocks pages.
+int check_table(int64_t page_size, int64_t max_blocks) {
+    if (page_size < 16 || page_size > 65536 || page_size % 16 != 0) return KQ_ERR_UNSUPPORTED;
+    if (max_blocks < 0 || max_blocks > kMaxKvTokens || max_blocks * page_size > kMaxKvTokens) return KQ_ERR_INVALID_ARG;
+    return KQ_OK;
+}
+
+// Head counts and size of an attention call.
+int check_heads(int64_t n_heads, int64_t n_kv_heads, int64_t head_dim) {
+    if (n_kv_heads < 1 || n_heads < n_kv_heads || n_heads > 65536 || n_heads % n_kv_heads != 0) return KQ_ERR_INVALID_ARG;
+    if (head_dim < 64 || head_dim > 256 || head_dim % 64 != 0) return KQ_ERR_UNSUPPORTED;
+    return KQ_OK;
+}
+
+// A pool [n_pages, n_kv_heads, page_size, row] of q4_0 rows whose slots are
+// 32-bit.
+int check_pool(int type, int64_t n_kv_heads, int64_t head_dim, int64_t n_pages, int64_t page_size) {
+    if (type != KQ_Q4_0) return KQ_ERR_UNSUPPORTED;
+    const int rc = check_heads(n_kv_heads, n_kv_heads, head_dim);
+    if (rc) return rc;
+    if (page_size < 16 || page_size > 65536 || page_size % 16 != 0) return KQ_ERR_UNSUPPORTED;
+    if (n_pages < 0 || n_pages > (int64_t(1) << 31) - 1 || n_pages * page_size > (int64_t(1) << 31) - 1)
+        return KQ_ERR_INVALID_ARG;
+    return KQ_OK;
+}
 }  // namespace
 
 int record_cuda(cudaError_t e) {
@@ -283,6 +313,82 @@ int kq_gather_mix(const float* y, int64_t rows, int64_t n, const int32_t* inv_or
     if ((y && !aligned16(y)) || !aligned16(out)) return KQ_ERR_ALIGNMENT;
     return launch_gather_mix(y, rows, n, inv_order, scores, n_tokens, top_k, out, err_flag,
                              static_cast<cudaStream_t>(stream));
+}
+
+int kq_kv_plan(const int32_t* cached_lens, const int32_t* new_lens, int64_t n_seqs, int32_t page_size,
+               int32_t* block_table, int64_t max_blocks, const int32_t* free_pages, int64_t n_free,
+               const int32_t* taken, int32_t* taken_out, int32_t* seq_lens, int32_t* cu_new, int32_t* first_page,
+               int32_t* slot_map, int32_t* positions, int64_t cap, int32_t* err_flag, void* stream) {
+    if (n_seqs < 0 || n_seqs > (int64_t(1) << 20) || cap < 0 || cap > kMaxKvTokens) return KQ_ERR_INVALID_ARG;
+    if (n_free < 0 || n_free > kMaxKvTokens) return KQ_ERR_INVALID_ARG;
+    const int rc = check_table(page_size, max_blocks);
+    if (rc) return rc;
+    if (!taken || !taken_out || !cu_new || (cap > 0 && !slot_map) || (n_free > 0 && !free_pages)) return KQ_ERR_INVALID_ARG;
+    if (n_seqs > 0 && (!cached_lens || !new_lens || !seq_lens || !first_page || (max_blocks > 0 && !block_table)))
+        return KQ_ERR_INVALID_ARG;
+    return launch_kv_plan(cached_lens, new_lens, n_seqs, page_size, block_table, max_blocks, free_pages, n_free, taken,
+                          taken_out, seq_lens, cu_new, first_page, slot_map, positions, cap, err_flag,
+                          static_cast<cudaStream_t>(stream));
+}
+
+int kq_kv_append(int type, const void* k, const void* v, int in_type, int64_t n_tokens, int64_t k_stride,
+                 int64_t v_stride, int32_t n_kv_heads, int32_t head_dim, const int32_t* slot_map, void* k_pool,
+                 void* v_pool, int64_t n_pages, int32_t page_size, int32_t* err_flag, void* stream) {
+    int rc = check_pool(type, n_kv_heads, head_dim, n_pages, page_size);
+    if (rc) return rc;
+    if (in_type != KQ_F32 && in_type != KQ_BF16) return KQ_ERR_UNSUPPORTED;
+    if (n_tokens < 0 || n_tokens > kMaxKvTokens) return KQ_ERR_INVALID_ARG;
+    // 64 blocks of 32 values a CTA, and the grid's x extent
+    if (n_tokens * n_kv_heads > (int64_t(1) << 31)) return KQ_ERR_INVALID_ARG;
+    const int64_t row = static_cast<int64_t>(n_kv_heads) * head_dim;
+    const int64_t per16 = in_type == KQ_F32 ? 4 : 8;
+    if (k_stride < row || v_stride < row || k_stride > kMaxK || v_stride > kMaxK) return KQ_ERR_INVALID_ARG;
+    if (n_tokens == 0) return KQ_OK;
+    if (!k || !v || !slot_map || !k_pool || !v_pool) return KQ_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool) || k_stride % per16 || v_stride % per16)
+        return KQ_ERR_ALIGNMENT;
+    return launch_kv_append(k, v, in_type == KQ_F32, n_tokens, k_stride, v_stride, n_kv_heads, head_dim, slot_map,
+                            k_pool, v_pool, n_pages, page_size, err_flag, static_cast<cudaStream_t>(stream));
+}
+
+int kq_kv_attention_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_new, int64_t* bytes) {
+    if (!bytes) return KQ_ERR_INVALID_ARG;
+    const int rc = check_heads(n_heads, n_kv_heads, head_dim);
+    if (rc) return rc;
+    if (max_new < 1) return KQ_ERR_INVALID_ARG;
+    *bytes = kv_attention_workspace(n_heads, n_kv_heads, head_dim, max_new);
+    return KQ_OK;
+}
+
+int kq_kv_attention(int type, const uint16_t* q, int64_t n_tokens, int64_t q_stride, int32_t n_heads,
+                    int32_t n_kv_heads, int32_t head_dim, const int32_t* cu_new, const int32_t* seq_lens,
+                    int64_t n_seqs, int32_t max_new, const void* k_pool, const void* v_pool, int64_t n_pages,
+                    int32_t page_size, const int32_t* block_table, int64_t max_blocks, float scale, int32_t causal,
+                    int32_t window, uint16_t* out, void* workspace, int64_t workspace_bytes, int32_t* err_flag,
+                    void* stream) {
+    int rc = check_pool(type, n_kv_heads, head_dim, n_pages, page_size);
+    if (rc) return rc;
+    rc = check_heads(n_heads, n_kv_heads, head_dim);
+    if (rc) return rc;
+    rc = check_table(page_size, max_blocks);
+    if (rc) return rc;
+    if (n_tokens < 0 || n_tokens > kMaxKvTokens || n_seqs < 0 || n_seqs > (int64_t(1) << 20)) return KQ_ERR_INVALID_ARG;
+    // the rows of one key head are counted in 32 bits
+    if (n_tokens * (n_heads / n_kv_heads) > kMaxK - 256) return KQ_ERR_INVALID_ARG;
+    const int64_t row = static_cast<int64_t>(n_heads) * head_dim;
+    if (q_stride < row || q_stride > kMaxK || max_new < 1 || window < 0 || window > kMaxKvTokens) return KQ_ERR_INVALID_ARG;
+    if (!(scale - scale == 0.f)) return KQ_ERR_INVALID_ARG;   // finite
+    if (n_tokens == 0 || n_seqs == 0) return KQ_OK;
+    if (!q || !cu_new || !seq_lens || !out || !workspace || (n_pages > 0 && (!k_pool || !v_pool)) ||
+        (max_blocks > 0 && !block_table))
+        return KQ_ERR_INVALID_ARG;
+    if (workspace_bytes < kv_attention_workspace(n_heads, n_kv_heads, head_dim, max_new)) return KQ_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || !aligned16(k_pool) || !aligned16(v_pool) ||
+        q_stride % 8 != 0)
+        return KQ_ERR_ALIGNMENT;
+    KvAttention a{q, q_stride, n_tokens, n_heads, n_kv_heads, head_dim, cu_new, seq_lens, n_seqs, max_new, k_pool,
+                  v_pool, n_pages, page_size, block_table, max_blocks, scale, causal, window, out, workspace, err_flag};
+    return launch_kv_attention(a, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,845 @@
+// kq_kv_attention over a paged q4_0 cache, for steps of few tokens a sequence.
+//
+// One pass over the keys with a running maximum and sum: for the rows (token,
+// query head) that share one key head,
+//   o = sum_j 2^(y_j - m) v_j / sum_j 2^(y_j - m),  y_j = log2(e) scale q.k_j.
+// The wire blocks are never expanded to values.  The tensor cores take the
+// 4-bit codes as binary16 subnormals (code * 2^-24: two AND-masks turn four
+// packed codes into two operand words; mma.sync keeps subnormal operands
+// exact), keys as the rows of the A operand:
+//   S[key, row]  = sum over blocks of d(key, block) * ((code - 8) . q)   where
+//                  the -8 is the accumulator's start, -8 * sum of the block's q
+//   O[dim, row] += (code - 8)[dim, key] * (P d)[key, row]                 where
+//                  the -8 is one more MMA with a constant operand.
+// q is scaled by a power of two per row (as every decode kernel of this
+// library), so only P and P * d are rounded, to binary16, each by at most
+// 2^-11 of its value: P is held as 2^13 * P and d is divided by a power of
+// two near the largest |d| of the value rows seen so far, so that neither
+// the smallest P nor tiny or huge values leave binary16's range.  Maximum,
+// sum and both accumulators are fp32.
+//
+// Work is cut by keys, not by sequences: the tiles of 32 keys of all
+// (sequence, key head, 8 or 16 rows) segments form one list, and every CTA of
+// a grid that fills the GPU once takes an equal run of it, whatever the
+// lengths (found on the device from the lengths; the host reads nothing).  In
+// a CTA one warp reads the block table and issues bulk copies of 16- or
+// 32-key runs into a ring of stages; seven warps take the tiles in turn, each
+// with a maximum, sum and accumulator of its own, joined in shared memory at
+// the end of a segment.  A segment that spans CTAs leaves fp32 partial results
+// in the workspace, joined in list order by a second kernel: no atomics, the
+// same result on every run.
+//
+// Bound by HBM: 0.5625 bytes per cached value.
+#include "kq_kv.cuh"
+
+namespace kq {
+namespace {
+
+constexpr int kTile = 32;        // keys of a tile
+constexpr int kWarps = 7;        // consumer warps (with the producer: 8, so that two CTAs have 128 registers a thread)
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kMinTiles = 8;     // least tiles of a CTA's share
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct AttnParams {
+    const uint16_t* q;
+    int64_t q_stride;            // elements between tokens
+    uint16_t* out;               // [n_tokens, n_heads, D]
+    int n_tokens;
+    int n_heads, n_kv, group;
+    const int32_t* cu;
+    const int32_t* lens;
+    int n_seqs;
+    const uint8_t* kp;
+    const uint8_t* vp;
+    int n_pages, page;
+    const int32_t* table;
+    int max_blocks;
+    float scale;                 // times log2(e)
+    int causal, window;
+    float* part;                 // partial results, two slots a CTA
+    int n_ctas;
+    int32_t* err;
+    int* status;
+};
+
+// A sequence's share of the work.
+struct Seq {
+    int tok0, qlen, len;         // first token, tokens, keys
+    int lo;                      // first key any row sees
+    int t0, nt;                  // first tile, tiles of a segment
+    int rt;                      // row tiles
+};
+
+template <int R>
+__device__ __forceinline__ Seq seq_of(const AttnParams& p, int b) {
+    Seq s;
+    int c0 = p.cu[b], c1 = p.cu[b + 1];
+    c0 = c0 < 0 ? 0 : (c0 > p.n_tokens ? p.n_tokens : c0);
+    c1 = c1 < c0 ? c0 : (c1 > p.n_tokens ? p.n_tokens : c1);
+    s.tok0 = c0;
+    s.qlen = c1 - c0;
+    int len = p.lens[b];
+    const int most = p.max_blocks * p.page;
+    len = len < 0 ? 0 : (len > most ? most : len);
+    s.len = len;
+    int lo = 0;
+    if (p.window > 0) {
+        lo = len - s.qlen - p.window + 1;
+        lo = lo < 0 ? 0 : (lo > len ? len : lo);
+    }
+    s.lo = lo;
+    s.t0 = lo / kTile;
+    const int nt = (len + kTile - 1) / kTile - s.t0;
+    s.nt = nt < 1 ? 1 : nt;      // a segment without keys still writes its zeros
+    s.rt = static_cast<int>((static_cast<int64_t>(s.qlen) * p.group + R - 1) / R);
+    return s;
+}
+__device__ __forceinline__ int64_t units_of(const AttnParams& p, const Seq& s) {
+    return static_cast<int64_t>(s.nt) * s.rt * p.n_kv;
+}
+
+// A place in the list: sequence, key head, row tile and tile.
+struct Place {
+    int b, h, rt, tile;
+    int64_t left;                // units of the CTA's share from here on
+};
+
+// Whole list length and the place of the unit at `share * blockIdx`, by the
+// threads of warp 0 .. all; results through shared memory.
+template <int R>
+__device__ __forceinline__ int64_t list_total(const AttnParams& p, unsigned long long* sum) {
+    if (threadIdx.x == 0) *sum = 0;
+    __syncthreads();
+    int64_t mine = 0;
+    for (int b = threadIdx.x; b < p.n_seqs; b += blockDim.x) mine += units_of(p, seq_of<R>(p, b));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if ((threadIdx.x & 31) == 0 && mine) atomicAdd(sum, static_cast<unsigned long long>(mine));
+    __syncthreads();
+    return static_cast<int64_t>(*sum);
+}
+// One warp: the sequence that holds unit u and the units before it.
+template <int R>
+__device__ __forceinline__ int list_find(const AttnParams& p, int64_t u, int64_t& before) {
+    const int lane = threadIdx.x & 31;
+    int64_t base = 0;
+    for (int b0 = 0; b0 < p.n_seqs; b0 += 32) {
+        const int b = b0 + lane;
+        const int64_t n = b < p.n_seqs ? units_of(p, seq_of<R>(p, b)) : 0;
+        int64_t inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, base + inc > u);
+        if (over) {
+            const int l = __ffs(over) - 1;
+            before = base + __shfl_sync(0xffffffffu, inc - n, l);
+            return b0 + l;
+        }
+        base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    before = base;
+    return p.n_seqs;
+}
+__device__ __forceinline__ int64_t share_of(int64_t total, int n_ctas) {
+    const int64_t s = (total + n_ctas - 1) / n_ctas;
+    return s < kMinTiles ? kMinTiles : s;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t hmax2_u32(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// All ones in each half of x that is not zero.
+__device__ __forceinline__ uint32_t half_mask(uint32_t x) {
+    return ((x & 0xffffu) ? 0xffffu : 0u) | ((x >> 16) ? 0xffff0000u : 0u);
+}
+__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+template <int NB, int NT>
+struct Shape {
+    static constexpr int D = 32 * NB;
+    static constexpr int R = 8 * NT;                   // rows of a segment
+    static constexpr int RB = 18 * NB;                 // bytes of a row
+    static constexpr int kStage = 2 * kTile * RB;      // keys, then values
+    static constexpr bool two = NB * NT <= 4;          // two CTAs an SM
+    static constexpr int DP = D + 4;                   // joined rows, padded (bank conflicts)
+    static constexpr int kJoin = 4 * R * DP * 4;       // four buffers of fp32 rows
+    static constexpr int kHead = 1024 + 2 * kWarps * R * 4;
+    static constexpr int kBudget = (two ? 113 : 226) * 1024;
+    static constexpr int kFit = (kBudget - kHead - kJoin) / kStage;
+    static constexpr int NST = kFit > 32 ? 32 : kFit;
+    static constexpr int kSmem = kHead + kJoin + NST * kStage;
+    static constexpr int kSlot = R * D + 2 * R;        // floats of a partial result
+};
+
+template <int NB, int NT>
+__global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_kernel(const AttnParams p) {
+    using C = Shape<NB, NT>;
+    constexpr int R = C::R, RB = C::RB, NST = C::NST, D = C::D;
+    static_assert(NST >= 8, "a stage for every consumer warp");
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+    uint64_t* empty = full + 32;
+    uint32_t* vmask = reinterpret_cast<uint32_t*>(smem + 512);   // keys of the stage that are there
+    volatile int* abort_ = reinterpret_cast<volatile int*>(smem + 640);
+    unsigned long long* sum = reinterpret_cast<unsigned long long*>(smem + 648);
+    Place* place = reinterpret_cast<Place*>(smem + 656);
+    float* wm = reinterpret_cast<float*>(smem + 1024);   // [warp][R] maximum
+    float* wl = wm + kWarps * R;                         // [warp][R] sum
+    float* join = reinterpret_cast<float*>(smem + C::kHead);
+    const uint32_t ring = smem_u32(smem) + C::kHead + C::kJoin;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        *abort_ = 0;
+        fence_barrier_init();
+    }
+    pdl_launch();
+    pdl_wait();
+    const int64_t total = list_total<R>(p, sum);
+    const int64_t share = share_of(total, p.n_ctas);
+    const int64_t u0 = share * blockIdx.x;
+    if (u0 >= total) return;
+    if (warp == 0) {
+        int64_t before;
+        const int b = list_find<R>(p, u0, before);
+        const Seq s = seq_of<R>(p, b);
+        const int64_t off = u0 - before, seg = off / s.nt;
+        if (lane == 0) {
+            place->b = b;
+            place->h = static_cast<int>(seg / s.rt);
+            place->rt = static_cast<int>(seg % s.rt);
+            place->tile = static_cast<int>(off - seg * s.nt);
+            place->left = total - u0 < share ? total - u0 : share;
+        }
+    }
+    __syncthreads();
+    Place at = *place;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (*abort_) return false;
+        if (mbar_try_wait(bar, parity)) return true;
+        if (!mbar_wait(bar, parity, p.status)) {
+            *abort_ = 1;
+            return false;
+        }
+        return true;
+    };
+    // next segment of the list
+    auto advance = [&](Seq& s) {
+        at.tile = 0;
+        if (++at.rt == s.rt) {
+            at.rt = 0;
+            if (++at.h == p.n_kv) {
+                at.h = 0;
+                do {
+                    ++at.b;
+                    s = seq_of<R>(p, at.b);
+                } while (s.rt == 0);
+            }
+        }
+    };
+
+    if (warp == kWarps) {
+        // ------------------------------------------------ producer
+        uint32_t n = 0;   // tiles issued
+        Seq s = seq_of<R>(p, at.b);
+        while (at.left > 0) {
+            const int tiles = static_cast<int>(at.left < s.nt - at.tile ? at.left : s.nt - at.tile);
+            for (int i0 = 0; i0 < tiles; i0 += 32) {
+                // lane i looks up tile i0 + i: two runs of 16 keys
+                const int key0 = (s.t0 + at.tile + i0 + lane) * kTile;
+                int64_t off[2] = {0, 0};
+                uint32_t mask = 0;
+                int bad = 0;
+                if (i0 + lane < tiles) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int key = key0 + 16 * j;
+                        if (key >= s.len || key + 16 <= s.lo) continue;
+                        const int blk = key / p.page;
+                        const int pg = p.table[static_cast<int64_t>(at.b) * p.max_blocks + blk];
+                        if (pg < 0 || pg >= p.n_pages) {
+                            bad = KQ_DEV_BAD_RANGE;
+                            continue;
+                        }
+                        mask |= 0xffffu << (16 * j);
+                        off[j] = ((static_cast<int64_t>(pg) * p.n_kv + at.h) * p.page + (key - blk * p.page)) * RB;
+                    }
+                }
+                if (bad && p.err) atomicOr(p.err, bad);
+                const int cnt = tiles - i0 < 32 ? tiles - i0 : 32;
+                for (int k = 0; k < cnt; ++k, ++n) {
+                    if (lane == k) {
+                        const uint32_t st = n % NST;
+                        if (wait(&empty[st], ((n / NST) & 1) ^ 1)) {
+                            vmask[st] = mask;
+                            const uint32_t dst = ring + st * C::kStage;
+                            const uint32_t half = 16 * RB;
+                            mbar_arrive_expect_tx(&full[st], __popc(mask) * 2 * RB);
+#pragma unroll
+                            for (int kv = 0; kv < 2; ++kv) {
+                                const uint8_t* src = kv ? p.vp : p.kp;
+                                uint8_t* d = smem + (dst - smem_u32(smem)) + kv * kTile * RB;
+                                if (mask == 0xffffffffu && off[1] == off[0] + half) {
+                                    bulk_g2s(d, src + off[0], 2 * half, &full[st]);
+                                } else {
+                                    if (mask & 1u) bulk_g2s(d, src + off[0], half, &full[st]);
+                                    if (mask >> 31) bulk_g2s(d + half, src + off[1], half, &full[st]);
+                                }
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            at.left -= tiles;
+            if (at.left > 0) advance(s);
+        }
+        if (*abort_) {
+            // let copies in flight land before the CTA's shared memory goes
+            const uint64_t t0 = global_ns();
+            while (global_ns() - t0 < 2000000ull) __nanosleep(10000);
+        }
+        return;
+    }
+
+    // -------------------------------------------------- consumers
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t n0 = 0;             // tiles before this segment
+    Seq s = seq_of<R>(p, at.b);
+    int slot = 0;                // partial slot: 0 while in the share's first segment
+    while (at.left > 0) {
+        const int tiles = static_cast<int>(at.left < s.nt - at.tile ? at.left : s.nt - at.tile);
+        const bool whole = tiles == s.nt;
+        const int rows = s.qlen * p.group - at.rt * R;   // rows of this tile that exist (may exceed R)
+        // ---- q: operand words and the accumulators' start
+        uint32_t qb[NT][NB][4];
+        float qc[NT][NB][2];
+        float yscale[NT][2];
+        int hi[NT][2], lo[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = nt * 8 + g;
+            const int rr = at.rt * R + r, i = rr / p.group;
+            const bool there = r < rows;
+            const uint16_t* src = p.q + (s.tok0 + (there ? i : 0)) * p.q_stride +
+                                  static_cast<int64_t>(at.h * p.group + (there ? rr - i * p.group : 0)) * D;
+            uint2 w[NB][2];      // values of byte j's low nibble, high nibble (bf16)
+            uint32_t mx = 0;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                // the bytes of this lane's word: even blocks 4t+2..4t+5 and (t = 3) 0, 1, 14, 15;
+                // odd blocks 4t..4t+3
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const uint16_t* a = src + 32 * b + 16 * hf;
+                    if (b & 1) {
+                        w[b][hf] = *reinterpret_cast<const uint2*>(a + 4 * t);
+                    } else {
+                        w[b][hf].x = *reinterpret_cast<const uint32_t*>(a + (t == 3 ? 0 : 4 * t + 2));
+                        w[b][hf].y = *reinterpret_cast<const uint32_t*>(a + (t == 3 ? 14 : 4 * t + 4));
+                    }
+                    if (!there) w[b][hf] = make_uint2(0, 0);
+                    mx = __vmaxu2(mx, __vmaxu2(w[b][hf].x & 0x7fff7fffu, w[b][hf].y & 0x7fff7fffu));
+                }
+            }
+            mx = max(mx & 0xffffu, mx >> 16);
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            if (mx >= 0x7f80u && p.err) atomicOr(p.err, KQ_DEV_X_RANGE);
+            const int e = xscale_exp(mx, 13);
+            const float up = exp2_int(e);
+            float sums[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float v[8];      // lo of bytes 0..3, hi of bytes 0..3
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    v[4 * hf] = bf16lo_to_f32(w[b][hf].x) * up;
+                    v[4 * hf + 1] = bf16hi_to_f32(w[b][hf].x) * up;
+                    v[4 * hf + 2] = bf16lo_to_f32(w[b][hf].y) * up;
+                    v[4 * hf + 3] = bf16hi_to_f32(w[b][hf].y) * up;
+                }
+                // high nibbles enter the MMA as 16 * code
+                qb[nt][b][0] = pack_f16x2(v[0], v[2]);
+                qb[nt][b][1] = pack_f16x2(v[4] * 0.0625f, v[6] * 0.0625f);
+                qb[nt][b][2] = pack_f16x2(v[1], v[3]);
+                qb[nt][b][3] = pack_f16x2(v[5] * 0.0625f, v[7] * 0.0625f);
+                float a = 0.f;   // of the rounded operands
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    a += (f16lo_to_f32(qb[nt][b][k]) + f16hi_to_f32(qb[nt][b][k])) * (k & 1 ? 16.f : 1.f);
+                a += __shfl_xor_sync(0xffffffffu, a, 1);
+                a += __shfl_xor_sync(0xffffffffu, a, 2);
+                sums[b] = a * (-8.f / 16777216.f);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int from = 4 * (2 * t + c);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) qc[nt][b][c] = __shfl_sync(0xffffffffu, sums[b], from);
+                const int ec = __shfl_sync(0xffffffffu, e, from);
+                // 2^24 of the codes and 2^-e of the row, in two steps (e reaches 126)
+                yscale[nt][c] = p.scale * 16777216.f * exp2_int(-ec);
+                const int rc = at.rt * R + nt * 8 + 2 * t + c;
+                const int pos = s.len - s.qlen + rc / p.group;
+                hi[nt][c] = p.causal ? pos : s.len - 1;
+                lo[nt][c] = p.window > 0 ? pos - p.window + 1 : 0;
+            }
+        }
+        // keys that every row of the segment sees
+        const int pos0 = s.len - s.qlen + (at.rt * R) / p.group;
+        const int last_row = min(at.rt * R + R, s.qlen * p.group) - 1;
+        const int pos1 = s.len - s.qlen + last_row / p.group;
+        const int all_hi = p.causal ? min(pos0, s.len - 1) : s.len - 1;
+        const int all_lo = p.window > 0 ? pos1 - p.window + 1 : 0;
+
+        float o[2 * NB][NT][4];
+        float m[NT][2], l[NT][2];
+        int ve = -14;            // exponent of the value scale
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[i][nt][k] = 0.f;
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+        }
+
+        // this warp's tiles: list positions n with n % kWarps == warp
+        for (int i = static_cast<int>((warp + kWarps - n0 % kWarps) % kWarps); i < tiles; i += kWarps) {
+            const uint32_t n = n0 + i, st = n % NST;
+            if (!__all_sync(0xffffffffu, wait(&full[st], (n / NST) & 1))) continue;
+            const uint32_t kb = ring + st * C::kStage, vb = kb + kTile * RB;
+            const int key0 = (s.t0 + at.tile + i) * kTile;
+            const uint32_t there = vmask[st];
+            // key of row r of the j-th 16: strides that keep the eight rows of
+            // a load on different banks
+            auto tau = [](int j, int r) {
+                const int gg = r & 7, up = r >> 3;
+                if (NB == 4) return 16 * j + 2 * gg + up;
+                if (NB == 8) return 16 * j + r;
+                return 4 * gg + 2 * j + up;
+            };
+            // ---- S
+            float y[2][NT][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t r0 = kb + tau(j, g) * RB, r1 = kb + tau(j, g + 8) * RB;
+#pragma unroll
+                for (int bp = 0; bp < NB / 2; ++bp) {
+                    uint32_t cw[2][2];   // [block of the pair][row]
+                    float d[2][2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t a = (r ? r1 : r0) + 36 * bp;
+                        const uint32_t w0 = lds32(a), w4 = lds32(a + 16), wx = lds32(a + 4 + 4 * t);
+                        cw[1][r] = lds32(a + 20 + 4 * t);
+                        cw[0][r] = __byte_perm(w0, wx, t == 3 ? 0x5432 : 0x7654);
+                        d[0][r] = f16lo_to_f32(w0);
+                        d[1][r] = f16hi_to_f32(w4);
+                    }
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int b = 2 * bp + hf;
+                        const uint32_t c0 = cw[hf][0], c1 = cw[hf][1];
+                        const uint32_t e0 = c0 >> 8, e1 = c1 >> 8;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float acc[4] = {qc[nt][b][0], qc[nt][b][1], qc[nt][b][0], qc[nt][b][1]};
+                            mma_f16(acc, c0 & 0x000f000fu, c1 & 0x000f000fu, c0 & 0x00f000f0u, c1 & 0x00f000f0u,
+                                    qb[nt][b][0], qb[nt][b][1]);
+                            mma_f16(acc, e0 & 0x000f000fu, e1 & 0x000f000fu, e0 & 0x00f000f0u, e1 & 0x00f000f0u,
+                                    qb[nt][b][2], qb[nt][b][3]);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                y[j][nt][k] = b == 0 ? d[hf][k >> 1] * acc[k] : fmaf(d[hf][k >> 1], acc[k], y[j][nt][k]);
+                        }
+                    }
+                }
+            }
+            const bool edge = there != 0xffffffffu || key0 + kTile - 1 > all_hi || key0 < all_lo;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[j][nt][k] *= yscale[nt][k & 1];
+            if (edge) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int tk = tau(j, g + 8 * (k >> 1)), key = key0 + tk;
+                            const bool ok = key < s.len && key <= hi[nt][k & 1] && key >= lo[nt][k & 1] && ((there >> tk) & 1u);
+                            if (!ok) y[j][nt][k] = -INFINITY;
+                        }
+            }
+            // ---- value scales: pairs of keys 2t, 2t + 1 and 2t + 8, 2t + 9 of each 16
+            uint32_t dv[2][NB][2];
+            uint32_t dm = 0;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int up = 0; up < 2; ++up) {
+                    const int ka = tau(j, 2 * t + 8 * up), kc = tau(j, 2 * t + 1 + 8 * up);
+                    uint32_t keep = 0xffffffffu;
+                    if (edge) {
+                        const bool a = key0 + ka < s.len && ((there >> ka) & 1u), c = key0 + kc < s.len && ((there >> kc) & 1u);
+                        keep = (a ? 0xffffu : 0u) | (c ? 0xffff0000u : 0u);
+                    }
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const uint32_t x = lds_u16(vb + ka * RB + 18 * b), z = lds_u16(vb + kc * RB + 18 * b);
+                        dv[j][b][up] = (x | (z << 16)) & keep;
+                        dm = hmax2_u32(dm, dv[j][b][up] & 0x7fff7fffu);
+                    }
+                }
+            dm = hmax2_u32(dm, __shfl_xor_sync(0xffffffffu, dm, 1));
+            dm = hmax2_u32(dm, __shfl_xor_sync(0xffffffffu, dm, 2));
+            const uint32_t dmx = max(dm & 0xffffu, dm >> 16);
+            int ne = static_cast<int>(dmx >> 10) - 15;
+            ne = ne < -14 ? -14 : (ne > 14 ? 14 : ne);
+            // ---- running maximum
+            bool grow = ne > ve;
+            float mt[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v = fmaxf(fmaxf(y[0][nt][c], y[0][nt][c + 2]), fmaxf(y[1][nt][c], y[1][nt][c + 2]));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    mt[nt][c] = fmaxf(m[nt][c], v);
+                    grow |= mt[nt][c] > m[nt][c];
+                }
+            if (__any_sync(0xffffffffu, grow)) {
+                const int e = ne > ve ? ne : ve;
+                const float fe = exp2_int(ve - e);
+                ve = e;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float f = m[nt][c] == mt[nt][c] ? 1.f : ex2(m[nt][c] - mt[nt][c]);
+                        m[nt][c] = mt[nt][c];
+                        l[nt][c] *= f;
+#pragma unroll
+                        for (int k = 0; k < 2 * NB; ++k) {
+                            o[k][nt][c] *= f * fe;
+                            o[k][nt][c + 2] *= f * fe;
+                        }
+                    }
+            }
+            const uint32_t vs = static_cast<uint32_t>((15 - ve) << 10) * 0x10001u;   // 2^-ve
+            // ---- P (2^13 P, binary16), transposed into B operand words
+            uint32_t pb[2][NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float mm[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) mm[c] = m[nt][c] == -INFINITY ? 0.f : 13.f - m[nt][c];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float e[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        e[k] = ex2(y[j][nt][k] + mm[k & 1]);
+                        l[nt][k & 1] += e[k];
+                    }
+                    pb[j][nt][0] = movm(pack_f16x2(e[0], e[1]));
+                    pb[j][nt][1] = movm(pack_f16x2(e[2], e[3]));
+                }
+            }
+            // ---- O
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t ra = vb + tau(j, 2 * t) * RB, rb = vb + tau(j, 2 * t + 1) * RB;
+                const uint32_t rc = vb + tau(j, 2 * t + 8) * RB, rd = vb + tau(j, 2 * t + 9) * RB;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const uint32_t c = 18 * b + 2 + 2 * g;
+                    const uint32_t x = lds_u16(ra + c) | (lds_u16(rb + c) << 16);
+                    const uint32_t z = lds_u16(rc + c) | (lds_u16(rd + c) << 16);
+                    const uint32_t x8 = x >> 8, z8 = z >> 8;
+                    const uint32_t d0 = hmul2_u32(dv[j][b][0], vs), d1 = hmul2_u32(dv[j][b][1], vs);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint32_t b0 = hmul2_u32(pb[j][nt][0], d0), b1 = hmul2_u32(pb[j][nt][1], d1);
+                        if (edge) {   // a key this row does not see adds nothing, whatever its scale
+                            b0 &= half_mask(pb[j][nt][0]);
+                            b1 &= half_mask(pb[j][nt][1]);
+                        }
+                        // rows g, g + 8: dims 2g, 2g + 1 of the block's first (then second) 16
+                        mma_f16(o[2 * b][nt], x & 0x000f000fu, x8 & 0x000f000fu, z & 0x000f000fu, z8 & 0x000f000fu, b0, b1);
+                        mma_f16(o[2 * b][nt], 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, b0, b1);
+                        mma_f16(o[2 * b + 1][nt], x & 0x00f000f0u, x8 & 0x00f000f0u, z & 0x00f000f0u, z8 & 0x00f000f0u, b0, b1);
+                        mma_f16(o[2 * b + 1][nt], 0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u, b0, b1);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st]);
+        }
+
+        // ---- join the warps
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float v = l[nt][c];
+                v += __shfl_xor_sync(0xffffffffu, v, 4);
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                if (g == 0) {
+                    const int r = nt * 8 + 2 * t + c;
+                    wm[warp * R + r] = m[nt][c];
+                    wl[warp * R + r] = v;
+                }
+            }
+        bar_sync(1, 32 * kWarps);
+        float M[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int r = nt * 8 + 2 * t + c;
+                float v = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) v = fmaxf(v, wm[w * R + r]);
+                M[nt][c] = v;
+                // codes' 2^24, the second 16 dims' 1/16, the value scale
+                const float f = m[nt][c] == -INFINITY ? 0.f : ex2(m[nt][c] - v) * 16777216.f * exp2_int(ve);
+#pragma unroll
+                for (int k = 0; k < 2 * NB; ++k) {
+                    const float fk = k & 1 ? f * 0.0625f : f;
+                    o[k][nt][c] *= fk;
+                    o[k][nt][c + 2] *= fk;
+                }
+            }
+        // warps 4..6 leave theirs, warps 0..3 add
+        auto row_at = [&](int w, int k, int nt, int c) {
+            return reinterpret_cast<float2*>(join + (w * R + nt * 8 + 2 * t + c) * C::DP + 32 * (k >> 1) + 16 * (k & 1) + 2 * g);
+        };
+        if (warp >= 4) {
+#pragma unroll
+            for (int k = 0; k < 2 * NB; ++k)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) *row_at(warp - 4, k, nt, c) = make_float2(o[k][nt][c], o[k][nt][c + 2]);
+        }
+        bar_sync(1, 32 * kWarps);
+        if (warp < 4) {
+#pragma unroll
+            for (int k = 0; k < 2 * NB; ++k)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float2* q2 = row_at(warp, k, nt, c);
+                        const float2 v = warp + 4 < kWarps ? *q2 : make_float2(0.f, 0.f);
+                        *q2 = make_float2(v.x + o[k][nt][c], v.y + o[k][nt][c + 2]);
+                    }
+        }
+        bar_sync(1, 32 * kWarps);
+        // sum of the four buffers: the output, or this CTA's partial result
+        float* part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * C::kSlot;
+        for (int i = tid; i < R * (D / 4); i += 32 * kWarps) {
+            const int r = i / (D / 4), c4 = (i % (D / 4)) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float4 x = *reinterpret_cast<const float4*>(join + (w * R + r) * C::DP + c4);
+                v.x += x.x;
+                v.y += x.y;
+                v.z += x.z;
+                v.w += x.w;
+            }
+            float mx = -INFINITY, sm = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, wm[w * R + r]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)   // (a warp without a maximum has 0, or NaN from a q that is none)
+                sm += wm[w * R + r] == -INFINITY ? wl[w * R + r] : wl[w * R + r] * ex2(wm[w * R + r] - mx);
+            if (whole) {
+                if (r < rows) {
+                    const int rr = at.rt * R + r, ti = rr / p.group;
+                    const float inv = sm == 0.f ? 0.f : 1.f / sm;
+                    uint2 out;
+                    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * inv, v.y * inv);
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+                    out.x = *reinterpret_cast<const uint32_t*>(&a);
+                    out.y = *reinterpret_cast<const uint32_t*>(&b);
+                    const int64_t row = static_cast<int64_t>(s.tok0 + ti) * p.n_heads + at.h * p.group + (rr - ti * p.group);
+                    if (sm == 0.f) out = make_uint2(0, 0);   // no key is seen
+                    *reinterpret_cast<uint2*>(p.out + row * D + c4) = out;
+                }
+            } else {
+                *reinterpret_cast<float4*>(part + r * D + c4) = v;
+                if (c4 == 0) {
+                    part[R * D + r] = mx;
+                    part[R * D + R + r] = sm;
+                }
+            }
+        }
+        bar_sync(1, 32 * kWarps);   // join, wm and wl are free again
+        n0 += tiles;
+        at.left -= tiles;
+        slot = 1;
+        if (at.left > 0) advance(s);
+    }
+}
+
+// Joins the partial results of the segments that span CTAs, in list order: CTA
+// i takes the segment that the boundary between shares i - 1 and i cuts, if
+// that is the first boundary inside it; blockIdx.y takes 64 of the D values.
+template <int NB, int NT>
+__global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p) {
+    using C = Shape<NB, NT>;
+    constexpr int R = C::R, D = C::D;
+    __shared__ unsigned long long sum;
+    __shared__ int64_t found[2];
+    pdl_wait();
+    const int64_t total = list_total<R>(p, &sum);
+    const int64_t share = share_of(total, p.n_ctas);
+    const int64_t u = share * (static_cast<int64_t>(blockIdx.x) + 1);
+    if (u >= total) return;
+    if (threadIdx.x < 32) {
+        int64_t before;
+        const int b = list_find<R>(p, u, before);
+        if (threadIdx.x == 0) {
+            found[0] = b;
+            found[1] = before;
+        }
+    }
+    __syncthreads();
+    const int b = static_cast<int>(found[0]);
+    const Seq s = seq_of<R>(p, b);
+    const int64_t off = u - found[1], seg = off / s.nt;
+    const int64_t a = found[1] + seg * s.nt, e = a + s.nt;   // units of the segment
+    if (a == u || u - share > a) return;                     // not cut here, or cut before
+    const int h = static_cast<int>(seg / s.rt), rt = static_cast<int>(seg % s.rt);
+    const int c0 = static_cast<int>(a / share), c1 = static_cast<int>((e - 1) / share);
+    const int rows = s.qlen * p.group - rt * R;
+    auto slot = [&](int c) { return p.part + (static_cast<int64_t>(c) * 2 + (c > c0 || a == c * share ? 0 : 1)) * C::kSlot; };
+    for (int i = threadIdx.x; i < R * 16; i += blockDim.x) {
+        const int r = i / 16, c4 = static_cast<int>(blockIdx.y) * 64 + (i % 16) * 4;
+        if (r >= rows) continue;
+        float mx = -INFINITY;
+        for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, slot(c)[R * D + r]);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sm = 0.f;
+        for (int c = c0; c <= c1; ++c) {
+            const float* q = slot(c);
+            const float mc = q[R * D + r];
+            const float f = mc == -INFINITY ? 0.f : ex2(mc - mx);
+            sm += mc == -INFINITY ? q[R * D + R + r] : f * q[R * D + R + r];
+            const float4 x = *reinterpret_cast<const float4*>(q + r * D + c4);
+            v.x += f * x.x;
+            v.y += f * x.y;
+            v.z += f * x.z;
+            v.w += f * x.w;
+        }
+        const float inv = sm == 0.f ? 0.f : 1.f / sm;
+        const __nv_bfloat162 x = __floats2bfloat162_rn(v.x * inv, v.y * inv);
+        const __nv_bfloat162 z = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+        const int rr = rt * R + r, ti = rr / p.group;
+        const int64_t row = static_cast<int64_t>(s.tok0 + ti) * p.n_heads + h * p.group + (rr - ti * p.group);
+        *reinterpret_cast<uint2*>(p.out + row * D + c4) = sm == 0.f ? make_uint2(0, 0) :
+            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&z));
+    }
+}
+
+template <int NB, int NT>
+int launch_of(AttnParams p, cudaStream_t s) {
+    using C = Shape<NB, NT>;
+    p.n_ctas = device_sm_count() * (C::two ? 2 : 1);
+    static bool ready[64] = {};   // the attribute is set once a device
+    int dev = 0;
+    int rc = record_cuda(cudaGetDevice(&dev));
+    if (rc) return rc;
+    if (dev >= 64 || !ready[dev]) {
+        rc = record_cuda(cudaFuncSetAttribute(attn_kernel<NB, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+        if (rc) return rc;
+        if (dev < 64) ready[dev] = true;
+    }
+    rc = launch_pdl(attn_kernel<NB, NT>, dim3(static_cast<unsigned>(p.n_ctas)), kThreads, C::kSmem, s, p);
+    if (rc) return rc;
+    return launch_pdl(attn_join_kernel<NB, NT>, dim3(static_cast<unsigned>(p.n_ctas - 1), NB / 2), 128, 0, s, p);
+}
+
+// Rows of a segment: 8 where a sequence's rows of one key head fit, else 16.
+int rows_of(int max_new, int group) { return static_cast<int64_t>(max_new) * group <= 8 ? 8 : 16; }
+
+}  // namespace
+
+int64_t kv_attention_workspace(int n_heads, int n_kv, int head_dim, int max_new) {
+    const int r = rows_of(max_new, n_heads / n_kv);
+    const int ctas = device_sm_count() * 2;
+    return static_cast<int64_t>(ctas) * 2 * (r * head_dim + 2 * r) * 4;
+}
+
+int launch_kv_attention(const KvAttention& a, cudaStream_t s) {
+    AttnParams p{};
+    p.q = a.q;
+    p.q_stride = a.q_stride;
+    p.out = a.out;
+    p.n_tokens = static_cast<int>(a.n_tokens);
+    p.n_heads = a.n_heads;
+    p.n_kv = a.n_kv;
+    p.group = a.n_heads / a.n_kv;
+    p.cu = a.cu_new;
+    p.lens = a.seq_lens;
+    p.n_seqs = static_cast<int>(a.n_seqs);
+    p.kp = static_cast<const uint8_t*>(a.k_pool);
+    p.vp = static_cast<const uint8_t*>(a.v_pool);
+    p.n_pages = static_cast<int>(a.n_pages);
+    p.page = a.page_size;
+    p.table = a.block_table;
+    p.max_blocks = static_cast<int>(a.max_blocks);
+    p.scale = a.scale * kLog2e;
+    p.causal = a.causal;
+    p.window = a.window;
+    p.part = static_cast<float*>(a.workspace);
+    p.err = a.err_flag;
+    p.status = device_status_ptr();
+    const bool small = rows_of(a.max_new, p.group) == 8;
+    switch (a.head_dim / 32) {
+    case 2: return small ? launch_of<2, 1>(p, s) : launch_of<2, 2>(p, s);
+    case 4: return small ? launch_of<4, 1>(p, s) : launch_of<4, 2>(p, s);
+    case 6: return small ? launch_of<6, 1>(p, s) : launch_of<6, 2>(p, s);
+    case 8: return small ? launch_of<8, 1>(p, s) : launch_of<8, 2>(p, s);
+    default: return KQ_ERR_UNSUPPORTED;
+    }
+}
+
+}  // namespace kq

@@ -57,4 +57,33 @@ int launch_gather_mix(const float* y, int64_t rows, int64_t n, const int32_t* in
 int launch_tile_map(const uint32_t* sorted_ids, int64_t rows, int n_experts, uint32_t* map, int64_t cap,
                     uint32_t* count, int32_t* err_flag, cudaStream_t s);
 
+// ---- KV cache in q4_0 pages (kq_kv.cu, kq_kv_attn.cu)
+int launch_kv_plan(const int32_t* cached_lens, const int32_t* new_lens, int64_t n_seqs, int page_size,
+                   int32_t* block_table, int64_t max_blocks, const int32_t* free_pages, int64_t n_free,
+                   const int32_t* taken, int32_t* taken_out, int32_t* seq_lens, int32_t* cu_new, int32_t* first_page,
+                   int32_t* slot_map, int32_t* positions, int64_t cap, int32_t* err_flag, cudaStream_t s);
+int launch_kv_append(const void* k, const void* v, int f32, int64_t n_tokens, int64_t k_stride, int64_t v_stride,
+                     int n_heads, int head_dim, const int32_t* slot_map, void* k_pool, void* v_pool, int64_t n_pages,
+                     int page_size, int32_t* err_flag, cudaStream_t s);
+struct KvAttention {
+    const uint16_t* q;
+    int64_t q_stride, n_tokens;
+    int n_heads, n_kv, head_dim;
+    const int32_t *cu_new, *seq_lens;
+    int64_t n_seqs;
+    int max_new;
+    const void *k_pool, *v_pool;
+    int64_t n_pages;
+    int page_size;
+    const int32_t* block_table;
+    int64_t max_blocks;
+    float scale;
+    int causal, window;
+    uint16_t* out;
+    void* workspace;
+    int32_t* err_flag;
+};
+int64_t kv_attention_workspace(int n_heads, int n_kv, int head_dim, int max_new);
+int launch_kv_attention(const KvAttention& a, cudaStream_t s);
+
 }  // namespace kq

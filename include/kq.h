@@ -337,6 +337,122 @@ int kq_gather_mix(const float* y, int64_t rows, int64_t n, const int32_t* inv_or
                   const float* scores, int64_t n_tokens, int32_t top_k, float* out,
                   int32_t* err_flag, void* stream);
 
+/*
+ * KV cache in q4_0 pages
+ * ----------------------
+ * Three calls make a step of a server between the products: kq_kv_plan (once
+ * a step: offsets, pages and slots from the requests' lengths, on the device),
+ * kq_kv_append (every layer: new keys and values into the cache) and
+ * kq_kv_attention (every layer: attention over the cache).  No counterpart on
+ * the pages, which stop at the weights.
+ *
+ * A pool is [n_pages, n_kv_heads, page_size, row] bytes, one for keys and one
+ * for values; a row is one token's head_dim values of one head as q4_0 wire
+ * blocks, row = head_dim / 32 * 18 bytes, so kq_dequantize(KQ_Q4_0) reads a
+ * pool back.  head_dim is 64, 128, 192 or 256 and page_size a multiple of 16
+ * up to 65536, else KQ_ERR_UNSUPPORTED; n_pages * page_size <= 2^31 - 1.  A
+ * slot is page * page_size + offset in the page.  Pools may hold anything
+ * where no token was written: what is not visible is never used.
+ */
+
+/* ggml type ids of plain values (inputs of kq_kv_append). */
+#define KQ_F32  0
+#define KQ_BF16 30
+
+/*
+ * kq_kv_plan - from the requests' lengths, on the device and without a host
+ * round trip: token offsets, lengths after the step, the pages that the new
+ * tokens need, and the slot and position of every new token.
+ *   cached_lens [n_seqs] int32   tokens a request already has in the cache
+ *   new_lens    [n_seqs] int32   tokens it adds in this step (0: idle)
+ *   block_table [n_seqs, max_blocks] int32, in and out: page of every
+ *               page_size tokens.  The first ceil(cached / page_size) entries
+ *               of a row are read, those of the pages taken in this step are
+ *               written, the others are left as they are.
+ *   free_pages  [n_free] int32   pages to take, in this order
+ *   taken, taken_out [1] int32   how many of them are taken before and after
+ *               the call (may be the same word)
+ *   seq_lens    [n_seqs] int32 out: cached + new (may be cached_lens)
+ *   cu_new      [n_seqs + 1] int32 out: exclusive sums of the new lengths
+ *   first_page  [n_seqs] int32 out: place in free_pages of the request's first
+ *               fresh page (work space of the call)
+ *   slot_map    [cap] int32 out: slot of token t of the step (the tokens of
+ *               request 0, then of request 1, ...), -1 for cu_new[n_seqs] <= t < cap
+ *   positions   [cap] int32 out (nullable): its place in its sequence, -1 behind the last
+ * Pages go to requests in order.  What does not fit is cut off and flagged in
+ * err_flag (nullable) with KQ_DEV_TOO_MANY: tokens past `cap` are dropped from
+ * the lengths, tokens past a table row or past the free pages keep their place
+ * but get slot -1 (and table entry -1).  Negative lengths count as 0, cached
+ * lengths past the row are cut, pages below 0 or past 32-bit slots give slot
+ * -1: KQ_DEV_BAD_RANGE.  n_seqs <= 2^20, cap, n_free and max_blocks *
+ * page_size <= 2^30.
+ */
+int kq_kv_plan(const int32_t* cached_lens, const int32_t* new_lens, int64_t n_seqs, int32_t page_size,
+               int32_t* block_table, int64_t max_blocks, const int32_t* free_pages, int64_t n_free,
+               const int32_t* taken, int32_t* taken_out, int32_t* seq_lens, int32_t* cu_new, int32_t* first_page,
+               int32_t* slot_map, int32_t* positions, int64_t cap, int32_t* err_flag, void* stream);
+
+/*
+ * kq_kv_append - encode the keys and values of n_tokens tokens into their
+ * slots.
+ *   type        KQ_Q4_0 (else KQ_ERR_UNSUPPORTED)
+ *   k, v        [n_tokens, n_kv_heads, head_dim] of in_type KQ_F32 (a product's
+ *               output) or KQ_BF16; token rows k_stride, v_stride elements
+ *               apart (>= n_kv_heads * head_dim, a multiple of 16 bytes)
+ *   slot_map    [n_tokens] int32: -1 leaves the token out; other slots outside
+ *               the pool are left out and flagged KQ_DEV_BAD_RANGE.  Where two
+ *               tokens have one slot, each of its blocks holds one of the two.
+ * Encoding, per block of 32 values, each step in fp32: d = -m / 8, m the value
+ * of largest magnitude (the first of equals), stored as binary16; codes
+ * min(15, trunc(x * (1 / d) + 8.5)); a block whose stored d is 0 has codes 8.
+ * A block with a non-finite value, or whose d leaves binary16's range, stores
+ * an infinite or NaN d and sets KQ_DEV_X_RANGE.  No other slot is touched.
+ */
+int kq_kv_append(int type, const void* k, const void* v, int in_type, int64_t n_tokens, int64_t k_stride,
+                 int64_t v_stride, int32_t n_kv_heads, int32_t head_dim, const int32_t* slot_map, void* k_pool,
+                 void* v_pool, int64_t n_pages, int32_t page_size, int32_t* err_flag, void* stream);
+
+/* Bytes of work space that kq_kv_attention needs on the current device (host
+ * call).  It depends on nothing but these arguments, and a larger max_new
+ * never needs less. */
+int kq_kv_attention_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_new, int64_t* bytes);
+
+/*
+ * kq_kv_attention - softmax(scale * q . K^T + mask) . V over the cache, for
+ * prompts, single tokens and anything between, in one ragged batch.
+ *   q           [n_tokens, n_heads, head_dim] bf16, token rows q_stride
+ *               elements apart (a multiple of 8); tokens cu_new[b] ..
+ *               cu_new[b + 1] - 1 are the last ones of sequence b
+ *   cu_new      [n_seqs + 1] int32, seq_lens [n_seqs] int32 (device; as
+ *               kq_kv_plan writes them): keys of sequence b, its own new
+ *               tokens among them (append first)
+ *   max_new     the largest number of new tokens of a sequence (host): chooses
+ *               kernels, never the result's meaning
+ *   block_table [n_seqs, max_blocks]; a page outside [0, n_pages) that holds
+ *               visible keys sets KQ_DEV_BAD_RANGE in err_flag (nullable) and
+ *               its keys count as hidden
+ *   causal      != 0: the token at position p (seq_len - new + i) sees the keys
+ *               j <= p; 0: all keys of its sequence
+ *   window      > 0: and only j > p - window; pages wholly before that are
+ *               not read
+ *   out         [n_tokens, n_heads, head_dim] bf16, dense; rows of tokens
+ *               that belong to no sequence are left as they are; a token that
+ *               sees no key gets zeros
+ *   workspace   device memory, at least kq_kv_attention_workspace bytes;
+ *               calls that may run at the same time need one each.  Nothing
+ *               in it has to be kept or cleared between calls.
+ * Query head h reads key head h / (n_heads / n_kv_heads).  Scores, softmax
+ * statistics and outputs are accumulated in fp32; probabilities are rounded to
+ * binary16.  Deterministic (no atomics on data).  A non-finite q sets
+ * KQ_DEV_X_RANGE.  n_tokens <= 2^30, n_seqs <= 2^20, window <= 2^30.
+ */
+int kq_kv_attention(int type, const uint16_t* q, int64_t n_tokens, int64_t q_stride, int32_t n_heads,
+                    int32_t n_kv_heads, int32_t head_dim, const int32_t* cu_new, const int32_t* seq_lens,
+                    int64_t n_seqs, int32_t max_new, const void* k_pool, const void* v_pool, int64_t n_pages,
+                    int32_t page_size, const int32_t* block_table, int64_t max_blocks, float scale, int32_t causal,
+                    int32_t window, uint16_t* out, void* workspace, int64_t workspace_bytes, int32_t* err_flag,
+                    void* stream);
+
 #ifdef __cplusplus
 }
 #endif
