@@ -34,4 +34,42 @@ int launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, A.
     return record_cuda(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+// An attention call as its kernels take it.
+struct AttnParams {
+    const uint16_t* q;
+    int64_t q_stride;            // elements between tokens
+    uint16_t* out;               // [n_tokens, n_heads, D]
+    int n_tokens;
+    int n_heads, n_kv, group;
+    const int32_t* cu;
+    const int32_t* lens;
+    int n_seqs;
+    const uint8_t* kp;
+    const uint8_t* vp;
+    int n_pages, page;
+    const int32_t* table;
+    int max_blocks;
+    float scale;                 // times log2(e)
+    int causal, window;
+    float* part;                 // partial results, two slots a CTA
+    int n_ctas;
+    int few;                     // sequences of at most this many rows a key head go to the few-row kernel
+    int32_t* err;
+    int* status;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The prompt kernel (kq_kv_prompt.cu) on tcgen05: head sizes that it covers,
+// its work space and its launch.
+bool kv_prompt_covers(int head_dim);
+int64_t kv_prompt_workspace(int head_dim);
+int launch_kv_prompt(AttnParams p, int head_dim, cudaStream_t s);
+
 }  // namespace kq

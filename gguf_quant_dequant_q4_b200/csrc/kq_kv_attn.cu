@@ -39,29 +39,6 @@ constexpr int kTile = 32;        // keys of a tile
 constexpr int kWarps = 7;        // consumer warps (with the producer: 8, so that two CTAs have 128 registers a thread)
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kMinTiles = 8;     // least tiles of a CTA's share
-constexpr float kLog2e = 1.4426950408889634f;
-
-struct AttnParams {
-    const uint16_t* q;
-    int64_t q_stride;            // elements between tokens
-    uint16_t* out;               // [n_tokens, n_heads, D]
-    int n_tokens;
-    int n_heads, n_kv, group;
-    const int32_t* cu;
-    const int32_t* lens;
-    int n_seqs;
-    const uint8_t* kp;
-    const uint8_t* vp;
-    int n_pages, page;
-    const int32_t* table;
-    int max_blocks;
-    float scale;                 // times log2(e)
-    int causal, window;
-    float* part;                 // partial results, two slots a CTA
-    int n_ctas;
-    int32_t* err;
-    int* status;
-};
 
 // A sequence's share of the work.
 struct Seq {
@@ -92,7 +69,8 @@ __device__ __forceinline__ Seq seq_of(const AttnParams& p, int b) {
     s.t0 = lo / kTile;
     const int nt = (len + kTile - 1) / kTile - s.t0;
     s.nt = nt < 1 ? 1 : nt;      // a segment without keys still writes its zeros
-    s.rt = static_cast<int>((static_cast<int64_t>(s.qlen) * p.group + R - 1) / R);
+    const int rows = s.qlen * p.group;
+    s.rt = rows > p.few ? 0 : (rows + R - 1) / R;   // (more rows: the prompt kernel's)
     return s;
 }
 __device__ __forceinline__ int64_t units_of(const AttnParams& p, const Seq& s) {
@@ -149,11 +127,6 @@ __device__ __forceinline__ int64_t share_of(int64_t total, int n_ctas) {
     return s < kMinTiles ? kMinTiles : s;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ uint32_t movm(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -797,15 +770,23 @@ int launch_of(AttnParams p, cudaStream_t s) {
     return launch_pdl(attn_join_kernel<NB, NT>, dim3(static_cast<unsigned>(p.n_ctas - 1), NB / 2), 128, 0, s, p);
 }
 
+// Sequences with more rows a key head than this go to the prompt kernel.
+constexpr int kFew = 32;
+
 // Rows of a segment: 8 where a sequence's rows of one key head fit, else 16.
 int rows_of(int max_new, int group) { return static_cast<int64_t>(max_new) * group <= 8 ? 8 : 16; }
+bool has_prompts(int head_dim, int max_new, int group) {
+    return kv_prompt_covers(head_dim) && static_cast<int64_t>(max_new) * group > kFew;
+}
 
 }  // namespace
 
 int64_t kv_attention_workspace(int n_heads, int n_kv, int head_dim, int max_new) {
     const int r = rows_of(max_new, n_heads / n_kv);
     const int ctas = device_sm_count() * 2;
-    return static_cast<int64_t>(ctas) * 2 * (r * head_dim + 2 * r) * 4;
+    const int64_t few = static_cast<int64_t>(ctas) * 2 * (r * head_dim + 2 * r) * 4;
+    const int64_t more = has_prompts(head_dim, max_new, n_heads / n_kv) ? kv_prompt_workspace(head_dim) : 0;
+    return few > more ? few : more;   // the kernels run one after the other
 }
 
 int launch_kv_attention(const KvAttention& a, cudaStream_t s) {
@@ -833,13 +814,17 @@ int launch_kv_attention(const KvAttention& a, cudaStream_t s) {
     p.err = a.err_flag;
     p.status = device_status_ptr();
     const bool small = rows_of(a.max_new, p.group) == 8;
+    const bool prompts = has_prompts(a.head_dim, a.max_new, p.group);
+    p.few = prompts ? kFew : 0x7fffffff;
+    int rc = KQ_ERR_UNSUPPORTED;
     switch (a.head_dim / 32) {
-    case 2: return small ? launch_of<2, 1>(p, s) : launch_of<2, 2>(p, s);
-    case 4: return small ? launch_of<4, 1>(p, s) : launch_of<4, 2>(p, s);
-    case 6: return small ? launch_of<6, 1>(p, s) : launch_of<6, 2>(p, s);
-    case 8: return small ? launch_of<8, 1>(p, s) : launch_of<8, 2>(p, s);
-    default: return KQ_ERR_UNSUPPORTED;
+    case 2: rc = small ? launch_of<2, 1>(p, s) : launch_of<2, 2>(p, s); break;
+    case 4: rc = small ? launch_of<4, 1>(p, s) : launch_of<4, 2>(p, s); break;
+    case 6: rc = small ? launch_of<6, 1>(p, s) : launch_of<6, 2>(p, s); break;
+    case 8: rc = small ? launch_of<8, 1>(p, s) : launch_of<8, 2>(p, s); break;
     }
+    if (rc || !prompts) return rc;
+    return launch_kv_prompt(p, a.head_dim, s);
 }
 
 }  // namespace kq

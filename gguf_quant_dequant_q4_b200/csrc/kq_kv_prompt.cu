@@ -1,0 +1,806 @@
+// kq_kv_attention for many rows a key head (prompts): tcgen05 tensor cores
+// over tiles of 256 rows x 128 keys.
+//
+// Rows are (token, query head of the key head's group) pairs, so one key head's
+// tile is decoded once for 256 rows.  Keys and values become binary16 values
+// (code - 8) * d in shared memory (one rounding, 2^-11), S = Q K^T and O += P V
+// accumulate in fp32 in tensor memory, P = 2^7 * 2^(y - m) goes back to tensor
+// memory as binary16 and is the second product's A operand.  The running
+// maximum m is only moved when a row's new one is more than 8 (a factor 2^8)
+// above it, so O is rescaled rarely; P stays below 2^15.
+//
+// Warp-specialized, one CTA an SM, 16 warps:
+//   warps 0..3, 4..7  softmax of rows 0..127 and 128..255 (thread = row): q into
+//                     shared memory, S from tensor memory, P back, the output
+//   warps 8..11       decoders: wire rows -> binary16 key and value tiles in the
+//                     128-byte-swizzled layout (thread = key; the tile of keys
+//                     is the K-major operand of Q K^T, the same layout of
+//                     values the MN-major operand of P V)
+//   warp 12           tcgen05.mma issuer and tensor memory allocator
+//   warp 13           block table and bulk copies of 16-key runs
+// The two halves alternate: while one half's softmax runs, the tensor cores
+// work on the other's P V and next Q K^T.  S and P share tensor memory: the
+// next Q K^T of a half is issued after its P V, and MMAs complete in order.
+// The order of the 32 values inside a block is whatever the code masks give;
+// q is stored in the same order and the output is put back in registers.
+//
+// Work is the list of (sequence, key head, 256 rows, 128 keys) tiles that the
+// causal mask and window leave, cut into equal runs, one a CTA, as in the
+// few-row kernel; a segment that spans CTAs leaves fp32 partial results.
+#include "kq_kv.cuh"
+
+namespace kq {
+namespace {
+
+constexpr int kRows = 256, kKeys = 128;
+constexpr int kThreads = 512;
+constexpr int kRaw = 3;            // raw tiles in flight
+constexpr int kMinShare = 4;       // least tiles of a CTA's share
+constexpr float kPBias = 7.f, kLazy = 8.f;
+
+// ---------------------------------------------------------------- PTX glue
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+// A and B from shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// A from tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+#define KQ_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), \
+                    "=r"(v[i + 6]), "=r"(v[i + 7])
+#define KQ_I8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), \
+                    "r"(v[i + 6]), "r"(v[i + 7])
+// 32 columns of this warp's 32 lanes; the wait is part of the statement, so
+// that no use of the registers can move before it.
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : KQ_R8(v, 0), KQ_R8(v, 8), KQ_R8(v, 16), KQ_R8(v, 24)
+        : "r"(a)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld64(uint32_t a, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, "
+        "%38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, "
+        "%60, %61, %62, %63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : KQ_R8(v, 0), KQ_R8(v, 8), KQ_R8(v, 16), KQ_R8(v, 24), KQ_R8(v, 32), KQ_R8(v, 40), KQ_R8(v, 48), KQ_R8(v, 56)
+        : "r"(a)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
+        KQ_I8(v, 0), KQ_I8(v, 8), KQ_I8(v, 16), KQ_I8(v, 24)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// Two fp32 at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// 128-byte swizzle, rows of 128 bytes in groups of 8 (1024 bytes).  As a
+// K-major operand (rows = M or N) the leading offset is unused; as an MN-major
+// operand (rows = K, 64 N values a row) it is the distance to the next 64 N
+// values, `next64`.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t next64) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (static_cast<uint64_t>(next64 >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(2) << 61);
+}
+// kind::f16: D fp32, A and B binary16, M = 128; B K-major or MN-major.
+__device__ __forceinline__ constexpr uint32_t idesc_of(int n, bool b_mn) {
+    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+
+// ---------------------------------------------------- order inside a block
+// 16-byte chunk c of a row holds the eight values of one 32-bit word of codes:
+// chunk 4b + i is word i of block b, whose bytes are (even blocks, 2 bytes off
+// a word) 4i + 2 .. 4i + 5 and, for i = 3, 0, 1, 14, 15; (odd blocks) 4i .. 4i + 3.
+__device__ __forceinline__ constexpr int byte_of(int b, int i, int k) {
+    return (b & 1) ? 4 * i + k : (i < 3 ? 4 * i + 2 + k : (k < 2 ? k : 12 + k));
+}
+// Value index (0..31) of element e of word i: bytes 0, 2 low, 0, 2 high, 1, 3
+// low, 1, 3 high.
+__device__ __forceinline__ constexpr int value_of(int b, int i, int e) {
+    const int k = 2 * (e & 1) + (e >> 2);
+    return byte_of(b, i, k) + ((e & 2) ? 16 : 0);
+}
+
+struct Seq {
+    int tok0, qlen, len, rows;
+};
+__device__ __forceinline__ Seq seq_of(const AttnParams& p, int b) {
+    Seq s;
+    int c0 = p.cu[b], c1 = p.cu[b + 1];
+    c0 = c0 < 0 ? 0 : (c0 > p.n_tokens ? p.n_tokens : c0);
+    c1 = c1 < c0 ? c0 : (c1 > p.n_tokens ? p.n_tokens : c1);
+    s.tok0 = c0;
+    s.qlen = c1 - c0;
+    int len = p.lens[b];
+    const int most = p.max_blocks * p.page;
+    s.len = len < 0 ? 0 : (len > most ? most : len);
+    s.rows = s.qlen * p.group;
+    return s;
+}
+// Key tiles [t0, t0 + n) that the rows of row tile rt see; at least one, so
+// that rows without keys are written.
+struct Span {
+    int t0, n, lo;
+};
+__device__ __forceinline__ Span span_of(const AttnParams& p, const Seq& s, int rt) {
+    const int first = s.len - s.qlen + rt * kRows / p.group;
+    const int end = min(rt * kRows + kRows, s.rows) - 1;
+    const int last = s.len - s.qlen + end / p.group;
+    int hi = p.causal ? last + 1 : s.len;     // one past the last key
+    hi = hi < 0 ? 0 : (hi > s.len ? s.len : hi);
+    int lo = p.window > 0 ? first - p.window + 1 : 0;
+    lo = lo < 0 ? 0 : (lo > hi ? hi : lo);
+    Span r;
+    r.lo = lo;
+    r.t0 = lo / kKeys;
+    const int n = (hi + kKeys - 1) / kKeys - r.t0;
+    r.n = n < 1 ? 1 : n;
+    return r;
+}
+// Tiles of a sequence for one key head.
+__device__ __forceinline__ int64_t tiles_of(const AttnParams& p, const Seq& s) {
+    if (s.rows <= p.few) return 0;
+    int64_t n = 0;
+    for (int rt = 0; rt * kRows < s.rows; ++rt) n += span_of(p, s, rt).n;
+    return n;
+}
+
+__device__ __forceinline__ int64_t list_total(const AttnParams& p, unsigned long long* sum) {
+    if (threadIdx.x == 0) *sum = 0;
+    __syncthreads();
+    int64_t mine = 0;
+    for (int b = threadIdx.x; b < p.n_seqs; b += blockDim.x) mine += tiles_of(p, seq_of(p, b)) * p.n_kv;
+    if (mine) atomicAdd(sum, static_cast<unsigned long long>(mine));
+    __syncthreads();
+    return static_cast<int64_t>(*sum);
+}
+__device__ __forceinline__ int64_t share_of(int64_t total, int n_ctas) {
+    const int64_t s = (total + n_ctas - 1) / n_ctas;
+    return s < kMinShare ? kMinShare : s;
+}
+
+// A place in the list, and the units before its segment.
+struct Place {
+    int b, h, rt, tile;
+    int64_t start;
+};
+// One warp: the place of unit u.
+__device__ __forceinline__ Place list_find(const AttnParams& p, int64_t u) {
+    const int lane = threadIdx.x & 31;
+    Place at{p.n_seqs, 0, 0, 0, 0};
+    int64_t base = 0;
+    for (int b0 = 0; b0 < p.n_seqs; b0 += 32) {
+        const int b = b0 + lane;
+        const int64_t per = b < p.n_seqs ? tiles_of(p, seq_of(p, b)) : 0;
+        const int64_t n = per * p.n_kv;
+        int64_t inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, base + inc > u);
+        if (over) {
+            const int l = __ffs(over) - 1;
+            const int64_t before = base + __shfl_sync(0xffffffffu, inc - n, l);
+            const int64_t pr = __shfl_sync(0xffffffffu, per, l);
+            at.b = b0 + l;
+            at.h = static_cast<int>((u - before) / pr);
+            at.start = before + at.h * pr;
+            const Seq s = seq_of(p, at.b);
+            for (;;) {
+                const int k = span_of(p, s, at.rt).n;
+                if (u < at.start + k) break;
+                at.start += k;
+                ++at.rt;
+            }
+            at.tile = static_cast<int>(u - at.start);
+            break;
+        }
+        base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    return at;
+}
+// The next segment of the list (there is one).
+__device__ __forceinline__ void advance(const AttnParams& p, Place& at, Seq& s) {
+    at.tile = 0;
+    ++at.rt;
+    if (at.rt * kRows >= s.rows) {
+        at.rt = 0;
+        if (++at.h == p.n_kv) {
+            at.h = 0;
+            do {
+                ++at.b;
+                s = seq_of(p, at.b);
+            } while (s.rows <= p.few);
+        }
+    }
+}
+
+template <int NB>
+struct Shape {
+    static constexpr int D = 32 * NB;
+    static constexpr int RB = 18 * NB;
+    static constexpr uint32_t kTileB = kKeys * D * 2;        // a key or value tile, a half of q
+    static constexpr uint32_t kHalfB = kKeys * 128;          // its first 64 values
+    static constexpr uint32_t kRawB = kKeys * RB;
+    static constexpr uint32_t kQ = 1024, kK = kQ + 2 * kTileB, kV = kK + 2 * kTileB, kRaw0 = kV + 2 * kTileB;
+    static constexpr uint32_t kSmem = kRaw0 + kRaw * kRawB + 1024;
+    static constexpr int kSlot = kRows * D + 2 * kRows;      // floats of a partial result
+};
+
+struct Bars {
+    uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t s_full[2], p_full[2], o_full[2], q_full[2];
+};
+
+template <int NB>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p) {
+    using C = Shape<NB>;
+    constexpr int D = C::D, RB = C::RB;
+    static_assert(C::kSmem <= 232448, "shared memory of a CTA");
+    extern __shared__ uint8_t smem_[];
+    uint8_t* smem = smem_ + ((1024u - (smem_u32(smem_) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(smem);
+    Bars& bar = *reinterpret_cast<Bars*>(smem);
+    static_assert(sizeof(Bars) <= 512, "barriers");
+    uint32_t* tmask = reinterpret_cast<uint32_t*>(smem + 512);           // [16] runs of a tile that are there
+    volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + 576);   // tensor memory, abort
+    unsigned long long* sum = reinterpret_cast<unsigned long long*>(smem + 592);
+    Place* place = reinterpret_cast<Place*>(smem + 608);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < kRaw; ++i) {
+            mbar_init(&bar.raw_full[i], 1);
+            mbar_init(&bar.raw_empty[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.k_full[i], 4);
+            mbar_init(&bar.k_empty[i], 1);
+            mbar_init(&bar.v_full[i], 4);
+            mbar_init(&bar.v_empty[i], 1);
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.p_full[i], 128);
+            mbar_init(&bar.o_full[i], 1);
+            mbar_init(&bar.q_full[i], 128);
+        }
+        misc[1] = 0;
+        fence_barrier_init();
+    }
+    pdl_launch();
+    pdl_wait();
+    const int64_t total = list_total(p, sum);
+    const int64_t share = share_of(total, p.n_ctas);
+    const int64_t u0 = share * blockIdx.x;
+    if (u0 >= total) return;
+    if (warp == 0) {
+        const Place at = list_find(p, u0);
+        if (lane == 0) *place = at;
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sb + 576));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    Place at = *place;
+    Seq s = seq_of(p, at.b);
+    int left = static_cast<int>(total - u0 < share ? total - u0 : share);
+    auto wait = [&](uint64_t* b, uint32_t parity) {
+        if (misc[1]) return false;
+        if (mbar_try_wait(b, parity)) return true;
+        if (!mbar_wait(b, parity, p.status)) {
+            misc[1] = 1;
+            return false;
+        }
+        return true;
+    };
+
+    if (warp >= 12) {
+        regs_dec<56>();
+        if (warp == 12) {
+            if (lane == 0) {
+                // -------------------------------------------- MMA issuer
+                constexpr uint32_t iqk = idesc_of(kKeys, false), ipv = idesc_of(D, true);
+                uint32_t n = 0;                          // tiles so far
+                uint32_t hn[2] = {0, 0}, hs[2] = {0, 0};   // tiles and segments of each half (the second may be idle)
+                while (left > 0) {
+                    const Span sp = span_of(p, s, at.rt);
+                    const int tiles = min(left, sp.n - at.tile);
+                    const int halves = s.rows - at.rt * kRows > 128 ? 2 : 1;
+                    bool ok = true;
+                    for (int i = 0; i < halves; ++i) ok = ok && wait(&bar.q_full[i], hs[i] & 1);
+                    auto qk = [&](int i, uint32_t m) {   // S of half i = q K^T, tile number m
+                        const uint64_t a = sw128_desc(sb + C::kQ + i * C::kTileB, 16);
+                        const uint64_t b = sw128_desc(sb + C::kK + (m & 1) * C::kTileB, 16);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t o = ((k >> 2) * C::kHalfB + (k & 3) * 32) >> 4;
+                            mma_ss(tmem + i * 128, a + o, b + o, iqk, k != 0);
+                        }
+                        tc_commit(&bar.s_full[i]);
+                    };
+                    ok = ok && wait(&bar.k_full[n & 1], (n >> 1) & 1);
+                    if (ok) {
+                        tc_fence_after();
+                        for (int i = 0; i < halves; ++i) qk(i, n);
+                        tc_commit(&bar.k_empty[n & 1]);
+                    }
+                    for (int j = 0; j < tiles; ++j, ++n) {
+                        const bool more = j + 1 < tiles;
+                        ok = ok && wait(&bar.v_full[n & 1], (n >> 1) & 1);
+                        for (int i = 0; i < halves; ++i) {
+                            ok = ok && wait(&bar.p_full[i], hn[i] & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t b = sw128_desc(sb + C::kV + (n & 1) * C::kTileB, C::kHalfB);
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                mma_ts(tmem + 256 + i * D, tmem + i * 128 + 8 * k, b + (k * 2048 >> 4), ipv, j + k != 0);
+                            if (more) {
+                                if (i == 0) ok = wait(&bar.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
+                                if (!ok) break;
+                                tc_fence_after();
+                                qk(i, n + 1);
+                            } else {
+                                tc_commit(&bar.o_full[i]);
+                            }
+                        }
+                        if (!ok) break;
+                        for (int i = 0; i < halves; ++i) ++hn[i];
+                        if (more) tc_commit(&bar.k_empty[(n + 1) & 1]);
+                        if (left - j > 1) tc_commit(&bar.v_empty[n & 1]);
+                    }
+                    if (!ok) break;
+                    for (int i = 0; i < halves; ++i) ++hs[i];
+                    left -= tiles;
+                    if (left > 0) advance(p, at, s);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 13) {
+            // ------------------------------------------------ loader
+            // raw tiles in the order K0, then K(j+1), V(j), over the share
+            uint32_t n = 0, r = 0;
+            auto load = [&](const uint8_t* pool, uint32_t mask, int64_t off) {
+                const uint32_t st = r % kRaw;
+                bool ok = true;
+                if (lane == 0) {
+                    ok = wait(&bar.raw_empty[st], ((r / kRaw) & 1) ^ 1);
+                    if (ok) mbar_arrive_expect_tx(&bar.raw_full[st], __popc(mask) * 16 * RB);
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (ok && ((mask >> lane) & 1u)) bulk_g2s(smem + C::kRaw0 + st * C::kRawB + lane * 16 * RB, pool + off, 16 * RB, &bar.raw_full[st]);
+                ++r;
+            };
+            uint32_t vmask = 0;    // of the tile whose values come next
+            int64_t voff = 0;
+            bool pending = false;
+            while (left > 0) {
+                const Span sp = span_of(p, s, at.rt);
+                const int tiles = min(left, sp.n - at.tile);
+                for (int j = 0; j < tiles; ++j, ++n) {
+                    // lane i < 8: keys 16 i .. of the tile
+                    const int key = (sp.t0 + at.tile + j) * kKeys + 16 * lane;
+                    int64_t off = 0;
+                    bool in = lane < 8 && key < s.len && key + 16 > sp.lo;
+                    if (in) {
+                        const int blk = key / p.page;
+                        const int pg = p.table[static_cast<int64_t>(at.b) * p.max_blocks + blk];
+                        if (pg < 0 || pg >= p.n_pages) {
+                            in = false;
+                            if (p.err) atomicOr(p.err, KQ_DEV_BAD_RANGE);
+                        } else {
+                            off = ((static_cast<int64_t>(pg) * p.n_kv + at.h) * p.page + (key - blk * p.page)) * RB;
+                        }
+                    }
+                    const uint32_t mask = __ballot_sync(0xffffffffu, in);
+                    if (lane == 0) tmask[n & 15] = mask;
+                    __syncwarp();
+                    load(p.kp, mask, off);
+                    if (pending) load(p.vp, vmask, voff);
+                    vmask = mask;
+                    voff = off;
+                    pending = true;
+                }
+                left -= tiles;
+                if (left > 0) advance(p, at, s);
+            }
+            if (pending) load(p.vp, vmask, voff);
+        }
+    } else if (warp >= 8) {
+        regs_dec<88>();
+        // ---------------------------------------------------- decoders
+        const int row = tid - 256;
+        uint32_t r = 0, n = 0;
+        const uint32_t sw = (row & 7) << 4;
+        // tile number m of `dst`, from raw tile r; the key is there or zero
+        auto decode = [&](uint32_t base, uint64_t* full, uint64_t* empty, uint32_t m, bool there) {
+            const uint32_t st = r % kRaw;
+            bool ok = wait(&bar.raw_full[st], (r / kRaw) & 1);
+            ok = wait(&empty[m & 1], ((m >> 1) & 1) ^ 1) && ok;
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                const uint32_t src = sb + C::kRaw0 + st * C::kRawB + row * RB;
+                uint32_t w[9 * NB / 2];
+                if constexpr (NB % 4 == 0) {
+#pragma unroll
+                    for (int i = 0; i < 9 * NB / 4; ++i) {
+                        const uint2 v = lds64(src + 8 * i);
+                        w[2 * i] = v.x;
+                        w[2 * i + 1] = v.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 9 * NB / 2; ++i) w[i] = lds32(src + 4 * i);
+                }
+                const uint32_t dst = base + (m & 1) * C::kTileB + row * 128;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const uint32_t* x = w + 9 * (b >> 1);
+                    uint32_t d = (b & 1) ? __byte_perm(x[4], x[4], 0x3232) : __byte_perm(x[0], x[0], 0x1010);
+                    if (!there) d = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t c = (b & 1) ? x[5 + i] : (i < 3 ? x[1 + i] : __byte_perm(x[0], x[4], 0x5432));
+                        const uint32_t e = c >> 8;
+                        // 1024 + code - 1032 and (1024 + 16 code) / 16 - 72: code - 8, exact
+                        const uint32_t v0 = hsub2_u32(and_or(c, 0x000f000fu, 0x64006400u), 0x64086408u);
+                        const uint32_t v1 = hfma2_u32(and_or(c, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
+                        const uint32_t v2 = hsub2_u32(and_or(e, 0x000f000fu, 0x64006400u), 0x64086408u);
+                        const uint32_t v3 = hfma2_u32(and_or(e, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
+                        const int ch = 4 * b + i;
+                        sts128(dst + (ch >> 3) * C::kHalfB + (((ch & 7) << 4) ^ sw), hmul2_u32(v0, d), hmul2_u32(v1, d),
+                               hmul2_u32(v2, d), hmul2_u32(v3, d));
+                    }
+                }
+                fence_proxy_async();
+            }
+            __syncwarp();
+            if (lane == 0 && ok) {
+                mbar_arrive(&bar.raw_empty[st]);
+                mbar_arrive(&full[m & 1]);
+            }
+            ++r;
+        };
+        bool pending = false, vthere = false;
+        while (left > 0) {
+            const Span sp = span_of(p, s, at.rt);
+            const int tiles = min(left, sp.n - at.tile);
+            for (int j = 0; j < tiles; ++j, ++n) {
+                const int key = (sp.t0 + at.tile + j) * kKeys + row;
+                // the loader's mask is read after its raw tile is full
+                const uint32_t st = r % kRaw;
+                wait(&bar.raw_full[st], (r / kRaw) & 1);
+                const bool there = key < s.len && ((reinterpret_cast<volatile uint32_t*>(tmask)[n & 15] >> (row >> 4)) & 1u);
+                decode(sb + C::kK, bar.k_full, bar.k_empty, n, there);
+                if (pending) decode(sb + C::kV, bar.v_full, bar.v_empty, n - 1, vthere);
+                vthere = there;
+                pending = true;
+            }
+            left -= tiles;
+            if (left > 0) advance(p, at, s);
+        }
+        if (pending) decode(sb + C::kV, bar.v_full, bar.v_empty, n - 1, vthere);
+    } else {
+        regs_inc<184>();
+        // ------------------------------------------------------ softmax
+        const int half = warp >> 2, row = tid & 127;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // this warp's 32 lanes of tensor memory
+        const uint32_t ts = tmem + half * 128 + lanes, to = tmem + 256 + half * D + lanes;
+        uint32_t n = 0;                // tiles so far
+        uint32_t hn = 0, hs = 0;       // tiles and segments of this half
+        int slot = 0;
+        while (left > 0) {
+            const Span sp = span_of(p, s, at.rt);
+            const int tiles = min(left, sp.n - at.tile);
+            const bool whole = tiles == sp.n;
+            const bool used = half == 0 || s.rows - at.rt * kRows > 128;
+            const int rr = at.rt * kRows + half * 128 + row;
+            const bool there = rr < s.rows;
+            const int ti = there ? rr / p.group : 0;
+            const int64_t qhead = static_cast<int64_t>(at.h) * p.group + (there ? rr - ti * p.group : 0);
+            const int pos = s.len - s.qlen + ti;
+            int hi = p.causal ? min(pos, s.len - 1) : s.len - 1;
+            int lo = p.window > 0 ? pos - p.window + 1 : 0;
+            if (!there) {
+                hi = 0x7fffffff;
+                lo = 0;
+            }
+            // ---- q: scaled by a power of two, in the blocks' order
+            float c = 1.f;       // of S, to base-2 scores
+            if (used) {
+                const uint16_t* src = p.q + (s.tok0 + ti) * p.q_stride + qhead * D;
+                uint32_t w[D / 2];
+                uint32_t mx = 0;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 v = there ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+                    w[4 * i] = v.x;
+                    w[4 * i + 1] = v.y;
+                    w[4 * i + 2] = v.z;
+                    w[4 * i + 3] = v.w;
+                    mx = absmax8_bf16(mx, v);
+                }
+                mx = max(mx & 0xffffu, mx >> 16);
+                if (mx >= 0x7f80u && p.err) atomicOr(p.err, KQ_DEV_X_RANGE);
+                const int e = xscale_exp(mx, 13);
+                // the scale's sign goes into q, so that c > 0; scale 0: q = 0
+                const float up = p.scale == 0.f ? 0.f : copysignf(exp2_int(e), p.scale);
+                c = p.scale == 0.f ? 1.f : fmaxf(fabsf(p.scale) * exp2_int(-e), 1.17549435e-38f);
+                const uint32_t dst = sb + C::kQ + half * C::kTileB + row * 128;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float f[2];
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                const int v = 32 * b + value_of(b, i, 2 * k + z);
+                                f[z] = ((v & 1) ? bf16hi_to_f32(w[v >> 1]) : bf16lo_to_f32(w[v >> 1])) * up;
+                            }
+                            o[k] = pack_f16x2(f[0], f[1]);
+                        }
+                        const int ch = 4 * b + i;
+                        sts128(dst + (ch >> 3) * C::kHalfB + (((ch & 7) << 4) ^ ((row & 7) << 4)), o[0], o[1], o[2], o[3]);
+                    }
+                fence_proxy_async();
+                tc_fence_before();
+                mbar_arrive(&bar.q_full[half]);
+            }
+            float m = -INFINITY;     // reference of the exponents, times c
+            float2 l2 = make_float2(0.f, 0.f);
+            for (int j = 0; used && j < tiles; ++j) {
+                if (!__all_sync(0xffffffffu, wait(&bar.s_full[half], (hn + j) & 1))) break;
+                tc_fence_after();
+                uint32_t x[128];
+                tmem_ld64(ts, x);
+                tmem_ld64(ts + 64, x + 64);
+                const int key0 = (sp.t0 + at.tile + j) * kKeys;
+                const uint32_t mask = reinterpret_cast<volatile uint32_t*>(tmask)[(n + j) & 15];
+                if (__any_sync(0xffffffffu, key0 + kKeys - 1 > hi || key0 < lo || mask != 0xffu)) {
+                    const int h0 = hi - key0, l0 = lo - key0;
+#pragma unroll
+                    for (int k = 0; k < 128; ++k)
+                        if (k > h0 || k < l0 || !((mask >> (k >> 4)) & 1u)) x[k] = 0xff800000u;
+                }
+                float mt = __uint_as_float(x[0]);
+#pragma unroll
+                for (int k = 1; k < 128; ++k) mt = fmaxf(mt, __uint_as_float(x[k]));
+                mt *= c;
+                if (__any_sync(0xffffffffu, mt > m + kLazy)) {
+                    const float nm = fmaxf(m, mt);
+                    const float f = m == nm ? 1.f : ex2(m - nm);
+                    m = nm;
+                    l2.x *= f;
+                    l2.y *= f;
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int k = 0; k < D / 32; ++k) {
+                            uint32_t o[32];
+                            tmem_ld32(to + 32 * k, o);
+#pragma unroll
+                            for (int z = 0; z < 32; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
+                            tmem_st32(to + 32 * k, o);
+                        }
+                    }
+                }
+                const float bias = m == -INFINITY ? 0.f : kPBias - m;
+                const float2 c2 = make_float2(c, c), b2 = make_float2(bias, bias);
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        float2 y = make_float2(__uint_as_float(x[64 * z + 2 * k]), __uint_as_float(x[64 * z + 2 * k + 1]));
+                        y = fma2(y, c2, b2);
+                        y.x = ex2(y.x);
+                        y.y = ex2(y.y);
+                        l2 = add2(l2, y);
+                        pk[k] = pack_f16x2(y.x, y.y);
+                    }
+                    tmem_st32(ts + 32 * z, pk);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&bar.p_full[half]);
+            }
+            // ---- output
+            const float l = l2.x + l2.y;
+            if (used && __all_sync(0xffffffffu, wait(&bar.o_full[half], hs & 1))) {
+                tc_fence_after();
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                float* part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * C::kSlot;
+                const int pr = half * 128 + row;
+                uint16_t* out = p.out + (static_cast<int64_t>(s.tok0 + ti) * p.n_heads + qhead) * D;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    uint32_t o[32];
+                    float v[32];
+                    tmem_ld32(to + 32 * b, o);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[value_of(b, i, e)] = __uint_as_float(o[8 * i + e]);
+                    if (whole) {
+                        if (there) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t h[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const __nv_bfloat162 t2 = __floats2bfloat162_rn(v[8 * i + 2 * k] * inv, v[8 * i + 2 * k + 1] * inv);
+                                    h[k] = l == 0.f ? 0u : *reinterpret_cast<const uint32_t*>(&t2);
+                                }
+                                *reinterpret_cast<uint4*>(out + 32 * b + 8 * i) = make_uint4(h[0], h[1], h[2], h[3]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<float4*>(part + pr * D + 32 * b + 4 * i) =
+                                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    }
+                }
+                if (!whole) {
+                    part[kRows * D + pr] = m;
+                    part[kRows * D + kRows + pr] = l;
+                }
+            }
+            n += tiles;
+            if (used) {
+                hn += tiles;
+                ++hs;
+            }
+            left -= tiles;
+            slot = 1;
+            if (left > 0) advance(p, at, s);
+        }
+    }
+    if (misc[1]) {   // let copies and MMAs in flight finish before the CTA's memory goes
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < 2000000ull) __nanosleep(10000);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// Joins the partial results of a segment that spans CTAs, in list order: the
+// first boundary between shares inside a segment takes it, 8 rows a block.
+template <int NB>
+__global__ void __launch_bounds__(256) prompt_join_kernel(const AttnParams p) {
+    using C = Shape<NB>;
+    constexpr int D = C::D, per = D / 4;
+    __shared__ unsigned long long sum;
+    __shared__ Place place;
+    pdl_wait();
+    const int64_t total = list_total(p, &sum);
+    const int64_t share = share_of(total, p.n_ctas);
+    const int64_t u = share * (static_cast<int64_t>(blockIdx.x) + 1);
+    if (u >= total) return;
+    if (threadIdx.x < 32) {
+        const Place at = list_find(p, u);
+        if (threadIdx.x == 0) place = at;
+    }
+    __syncthreads();
+    const Place at = place;
+    const Seq s = seq_of(p, at.b);
+    const int64_t a = at.start, e = a + span_of(p, s, at.rt).n;
+    if (a == u || u - share > a) return;   // not cut here, or cut before
+    const int c0 = static_cast<int>(a / share), c1 = static_cast<int>((e - 1) / share);
+    auto slot = [&](int c) { return p.part + (static_cast<int64_t>(c) * 2 + (c > c0 || a == c * share ? 0 : 1)) * C::kSlot; };
+    for (int i = threadIdx.x; i < 8 * per; i += 256) {
+        const int r = blockIdx.y * 8 + i / per, c4 = (i % per) * 4, rr = at.rt * kRows + r;
+        if (rr >= s.rows) continue;
+        float mx = -INFINITY;
+        for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, slot(c)[kRows * D + r]);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+        for (int c = c0; c <= c1; ++c) {
+            const float* q = slot(c);
+            const float mc = q[kRows * D + r], lc = q[kRows * D + kRows + r];
+            const float f = mc == -INFINITY ? 0.f : ex2(mc - mx);
+            l += mc == -INFINITY ? lc : f * lc;
+            const float4 x = *reinterpret_cast<const float4*>(q + r * D + c4);
+            v.x += f * x.x;
+            v.y += f * x.y;
+            v.z += f * x.z;
+            v.w += f * x.w;
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const __nv_bfloat162 x = __floats2bfloat162_rn(v.x * inv, v.y * inv);
+        const __nv_bfloat162 z = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+        const int ti = rr / p.group;
+        const int64_t row = static_cast<int64_t>(s.tok0 + ti) * p.n_heads + at.h * p.group + (rr - ti * p.group);
+        *reinterpret_cast<uint2*>(p.out + row * D + c4) = l == 0.f ? make_uint2(0, 0) :
+            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&z));
+    }
+}
+
+template <int NB>
+int launch_of(AttnParams p, cudaStream_t s) {
+    using C = Shape<NB>;
+    p.n_ctas = device_sm_count();
+    static bool ready[64] = {};   // the attribute is set once a device
+    int dev = 0;
+    int rc = record_cuda(cudaGetDevice(&dev));
+    if (rc) return rc;
+    if (dev >= 64 || !ready[dev]) {
+        rc = record_cuda(cudaFuncSetAttribute(prompt_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+        if (rc) return rc;
+        if (dev < 64) ready[dev] = true;
+    }
+    rc = launch_pdl(prompt_kernel<NB>, dim3(static_cast<unsigned>(p.n_ctas)), kThreads, C::kSmem, s, p);
+    if (rc || p.n_ctas == 1) return rc;
+    return launch_pdl(prompt_join_kernel<NB>, dim3(static_cast<unsigned>(p.n_ctas - 1), kRows / 8), 256, 0, s, p);
+}
+
+}  // namespace
+
+bool kv_prompt_covers(int head_dim) { return head_dim == 64 || head_dim == 128; }
+
+int64_t kv_prompt_workspace(int head_dim) {
+    return static_cast<int64_t>(device_sm_count()) * 2 * (kRows * head_dim + 2 * kRows) * 4;
+}
+
+int launch_kv_prompt(AttnParams p, int head_dim, cudaStream_t s) {
+    return head_dim == 64 ? launch_of<2>(p, s) : launch_of<4>(p, s);
+}
+
+}  // namespace kq

@@ -421,6 +421,55 @@ def test_few_tokens(seqs, hq, hkv, d, causal, window):
 
 
 @gpu
+@pytest.mark.parametrize("seqs", [[(300, 300)], [(200, 129), (77, 77), (40, 1), (0, 0), (513, 500), (33, 3)], [(2500, 70)],
+                                  [(1, 1), (700, 257), (128, 128), (1000, 33)], [(5000, 65), (64, 64), (129, 129)]])
+@pytest.mark.parametrize("hq,hkv,d,page", [(4, 4, 64, 16), (3, 1, 64, 48), (8, 2, 128, 32), (7, 1, 128, 16), (16, 1, 128, 64)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 100), (False, 0)])
+def test_prompts(seqs, hq, hkv, d, page, causal, window):
+    case = _kv.Case(seqs, hq, hkv, d, page, seed=11)
+    err = flag()
+    check(case, attend(case, d ** -0.5, causal, window, err=err), d ** -0.5, causal, window, wide=True)
+    assert int(err) == 0
+
+
+@gpu
+@pytest.mark.parametrize("hq,hkv,d", [(6, 2, 192), (8, 2, 256)])
+def test_prompts_of_wide_heads(hq, hkv, d):
+    case = _kv.Case([(150, 150), (300, 40), (17, 1)], hq, hkv, d, 32, seed=12)
+    check(case, attend(case, d ** -0.5, True, 50), d ** -0.5, True, 50)
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_rows_that_see_nothing_bad_pages_and_padding(d):
+    # more new tokens than keys, no keys at all, hidden pages, rows of no sequence
+    case = _kv.Case([(200, 200), (0, 40), (300, 150), (5, 1)], 4, 2, d, 16, seed=13, pad=5)
+    case.lens[0] = 90                              # its first 110 tokens are before key 0
+    hidden = [(2, 0), (2, 9), (2, 18)]
+    want = case.expected(0.2, True, 0, hidden)
+    for i, (b, j) in enumerate(hidden):
+        case.table[b, j] = (-1, case.n_pages, 2**31 - 1)[i]
+    out = torch.full((case.q.shape[0], 4, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    err = flag()
+    got = attend(case, 0.2, out=out, err=err)
+    assert int(err) == kq.DEV_BAD_RANGE
+    case.expected = lambda *a: want
+    check(case, got, 0.2, hidden=hidden, wide=True)
+    assert bool((got[:110] == 0).all()) and bool((got[200:240] == 0).all()) and bool((got[391:] == 5).all())
+
+
+@gpu
+@pytest.mark.parametrize("k_exp,v_exp,q_scale,scale", [
+    ((-4, -1), (-23, -20), 1.0, 0.1), ((-4, -1), (9, 12.5), 1.0, 0.1), ((-20, -18), (-4, 0), 1e5, 0.5),
+    ((8, 10), (-4, 0), 1e-6, 10.0), ((-4, -1), (-4, 0), 1e30, 1e-30), ((-4, -1), (-4, 0), 1.0, 0.0),
+    ((-4, -1), (-4, 0), 1.0, -0.2), ((-2, 0), (-4, 0), 8.0, 1.0),
+])
+def test_prompt_ranges(k_exp, v_exp, q_scale, scale):
+    case = _kv.Case([(333, 200), (600, 65)], 4, 2, 128, 16, seed=14, k_exp=k_exp, v_exp=v_exp, q_scale=q_scale)
+    check(case, attend(case, scale), scale, wide=True)
+
+
+@gpu
 def test_rows_that_see_nothing_and_rows_of_no_sequence():
     # a sequence without keys, and one with more new tokens than keys: zeros;
     # the padded rows behind the last sequence stay as they were
