@@ -133,18 +133,21 @@ __device__ __forceinline__ uint32_t movm(uint32_t x) {
     return y;
 }
 __device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    uint32_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
-__device__ __forceinline__ uint32_t hmax2_u32(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
+__device__ __forceinline__ void sts_u16(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(v)) : "memory");
 }
-// All ones in each half of x that is not zero.
-__device__ __forceinline__ uint32_t half_mask(uint32_t x) {
-    return ((x & 0xffffu) ? 0xffffu : 0u) | ((x >> 16) ? 0xffff0000u : 0u);
+// D = A B + C with C kept apart (fragments as mma_f16).
+__device__ __forceinline__ void mma_f16c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, const float (&c)[4]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
@@ -156,11 +159,16 @@ struct Shape {
     static constexpr int kStage = 2 * kTile * RB;      // keys, then values
     static constexpr bool two = NB * NT <= 4;          // two CTAs an SM
     static constexpr int DP = D + 4;                   // joined rows, padded (bank conflicts)
-    static constexpr int kJoin = 4 * R * DP * 4;       // four buffers of fp32 rows
-    static constexpr int kHead = 1024 + 2 * kWarps * R * 4;
+    static constexpr int kJoin = 3 * R * DP * 4;       // three buffers of fp32 rows
+    static constexpr int kScale = 64 * NB;             // a warp's value scales of a tile, in operand order
+    static constexpr int kHead = 1024 + 2 * kWarps * R * 4 + kWarps * kScale;
     static constexpr int kBudget = (two ? 113 : 226) * 1024;
     static constexpr int kFit = (kBudget - kHead - kJoin) / kStage;
-    static constexpr int NST = kFit > 32 ? 32 : kFit;
+    // A stage belongs to one consumer warp (NST a multiple of their number):
+    // were it shared, a warp could wait for a stage's next use before the use
+    // before it has landed (copies land in any order), and take that phase's
+    // parity for its own.
+    static constexpr int NST = (kFit > 32 ? 32 : kFit) / kWarps * kWarps;
     static constexpr int kSmem = kHead + kJoin + NST * kStage;
     static constexpr int kSlot = R * D + 2 * R;        // floats of a partial result
 };
@@ -169,7 +177,7 @@ template <int NB, int NT>
 __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_kernel(const AttnParams p) {
     using C = Shape<NB, NT>;
     constexpr int R = C::R, RB = C::RB, NST = C::NST, D = C::D;
-    static_assert(NST >= 8, "a stage for every consumer warp");
+    static_assert(NST >= kWarps && NST % kWarps == 0, "stages of its own for every consumer warp");
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);
     uint64_t* empty = full + 32;
@@ -179,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
     Place* place = reinterpret_cast<Place*>(smem + 656);
     float* wm = reinterpret_cast<float*>(smem + 1024);   // [warp][R] maximum
     float* wl = wm + kWarps * R;                         // [warp][R] sum
+    const uint32_t scales = smem_u32(smem) + 1024 + 2 * kWarps * R * 4 + (threadIdx.x >> 5) * C::kScale;
     float* join = reinterpret_cast<float*>(smem + C::kHead);
     const uint32_t ring = smem_u32(smem) + C::kHead + C::kJoin;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -238,56 +247,46 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
 
     if (warp == kWarps) {
         // ------------------------------------------------ producer
+        // Four lanes a tile (keys or values, first or second 16 keys), BT tiles
+        // at a time: their table entries, waits and copies overlap.
+        constexpr int BT = NST >= 16 ? 8 : 4;
         uint32_t n = 0;   // tiles issued
+        const int q = lane >> 2, kv = lane & 1, sl = (lane >> 1) & 1;
         Seq s = seq_of<R>(p, at.b);
         while (at.left > 0) {
             const int tiles = static_cast<int>(at.left < s.nt - at.tile ? at.left : s.nt - at.tile);
-            for (int i0 = 0; i0 < tiles; i0 += 32) {
-                // lane i looks up tile i0 + i: two runs of 16 keys
-                const int key0 = (s.t0 + at.tile + i0 + lane) * kTile;
-                int64_t off[2] = {0, 0};
-                uint32_t mask = 0;
-                int bad = 0;
-                if (i0 + lane < tiles) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int key = key0 + 16 * j;
-                        if (key >= s.len || key + 16 <= s.lo) continue;
-                        const int blk = key / p.page;
-                        const int pg = p.table[static_cast<int64_t>(at.b) * p.max_blocks + blk];
-                        if (pg < 0 || pg >= p.n_pages) {
-                            bad = KQ_DEV_BAD_RANGE;
-                            continue;
-                        }
-                        mask |= 0xffffu << (16 * j);
-                        off[j] = ((static_cast<int64_t>(pg) * p.n_kv + at.h) * p.page + (key - blk * p.page)) * RB;
+            // page of this lane's keys of tile i; -1: no visible key, -2: no such page
+            auto look = [&](int i) {
+                const int key = (s.t0 + at.tile + i) * kTile + 16 * sl;
+                if (q >= BT || i >= tiles || key >= s.len || key + 16 <= s.lo) return -1;
+                const int pg = p.table[static_cast<int64_t>(at.b) * p.max_blocks + key / p.page];
+                return pg < 0 || pg >= p.n_pages ? -2 : pg;
+            };
+            int next = look(q);
+            for (int i0 = 0; i0 < tiles; i0 += BT) {
+                const int pg = next, i = i0 + q;
+                next = look(i + BT);
+                if (pg == -2 && kv == 0 && p.err) atomicOr(p.err, KQ_DEV_BAD_RANGE);
+                const int key = (s.t0 + at.tile + i) * kTile + 16 * sl;
+                const int64_t off = ((static_cast<int64_t>(pg) * p.n_kv + at.h) * p.page + key % p.page) * RB;
+                const unsigned in = __ballot_sync(0xffffffffu, pg >= 0) >> (lane & 28);
+                const int64_t off0 = __shfl_sync(0xffffffffu, off, lane & 29), off1 = __shfl_sync(0xffffffffu, off, lane | 2);
+                const bool both = (in & 5u) == 5u && off1 == off0 + 16 * RB;   // one run of 32 keys
+                const uint32_t st = (n + q) % NST;
+                bool ok = q < BT && i < tiles;
+                if (ok && (lane & 3) == 0) {
+                    ok = wait(&empty[st], (((n + q) / NST) & 1) ^ 1);
+                    if (ok) {
+                        vmask[st] = ((in & 1u) ? 0xffffu : 0u) | ((in & 4u) ? 0xffff0000u : 0u);
+                        mbar_arrive_expect_tx(&full[st], ((in & 1u) + ((in >> 2) & 1u)) * 32 * RB);
                     }
                 }
-                if (bad && p.err) atomicOr(p.err, bad);
-                const int cnt = tiles - i0 < 32 ? tiles - i0 : 32;
-                for (int k = 0; k < cnt; ++k, ++n) {
-                    if (lane == k) {
-                        const uint32_t st = n % NST;
-                        if (wait(&empty[st], ((n / NST) & 1) ^ 1)) {
-                            vmask[st] = mask;
-                            const uint32_t dst = ring + st * C::kStage;
-                            const uint32_t half = 16 * RB;
-                            mbar_arrive_expect_tx(&full[st], __popc(mask) * 2 * RB);
-#pragma unroll
-                            for (int kv = 0; kv < 2; ++kv) {
-                                const uint8_t* src = kv ? p.vp : p.kp;
-                                uint8_t* d = smem + (dst - smem_u32(smem)) + kv * kTile * RB;
-                                if (mask == 0xffffffffu && off[1] == off[0] + half) {
-                                    bulk_g2s(d, src + off[0], 2 * half, &full[st]);
-                                } else {
-                                    if (mask & 1u) bulk_g2s(d, src + off[0], half, &full[st]);
-                                    if (mask >> 31) bulk_g2s(d + half, src + off[1], half, &full[st]);
-                                }
-                            }
-                        }
-                    }
-                    __syncwarp();
+                ok = __shfl_sync(0xffffffffu, ok, lane & 28);
+                if (ok && pg >= 0 && !(both && sl)) {
+                    uint8_t* d = smem + C::kHead + C::kJoin + st * C::kStage + (kv * kTile + sl * 16) * RB;
+                    bulk_g2s(d, (kv ? p.vp : p.kp) + off, both ? 32 * RB : 16 * RB, &full[st]);
                 }
+                n += tiles - i0 < BT ? tiles - i0 : BT;
             }
             at.left -= tiles;
             if (at.left > 0) advance(s);
@@ -302,6 +301,22 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
 
     // -------------------------------------------------- consumers
     const int g = lane >> 2, t = lane & 3;
+    // key of row r of the j-th 16 of a tile: strides that keep the eight rows
+    // of a load on different banks
+    auto tau = [](int j, int r) {
+        const int gg = r & 7, up = r >> 3;
+        if (NB == 4) return 16 * j + 2 * gg + up;
+        if (NB == 8) return 16 * j + r;
+        return 4 * gg + 2 * j + up;
+    };
+    // where key `lane` has its value scale: rows 2t', 2t' + 1, 2t' + 8, 2t' + 9
+    // of both 16s are the eight halves of t'
+    uint32_t scale_at = scales;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if (tau(j, r) == lane) scale_at += 16 * ((r & 7) >> 1) + 8 * j + 4 * (r >> 3) + 2 * (r & 1);
     uint32_t n0 = 0;             // tiles before this segment
     Seq s = seq_of<R>(p, at.b);
     int slot = 0;                // partial slot: 0 while in the share's first segment
@@ -311,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
         const int rows = s.qlen * p.group - at.rt * R;   // rows of this tile that exist (may exceed R)
         // ---- q: operand words and the accumulators' start
         uint32_t qb[NT][NB][4];
-        float qc[NT][NB][2];
+        float qc[NT][NB][4];
         float yscale[NT][2];
         int hi[NT][2], lo[NT][2];
 #pragma unroll
@@ -345,7 +360,8 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
             mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             if (mx >= 0x7f80u && p.err) atomicOr(p.err, KQ_DEV_X_RANGE);
             const int e = xscale_exp(mx, 13);
-            const float up = exp2_int(e);
+            // the scale's sign goes into q, so that yscale > 0; scale 0: q = 0
+            const float up = p.scale == 0.f ? 0.f : copysignf(exp2_int(e), p.scale);
             float sums[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
@@ -374,10 +390,10 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
             for (int c = 0; c < 2; ++c) {
                 const int from = 4 * (2 * t + c);
 #pragma unroll
-                for (int b = 0; b < NB; ++b) qc[nt][b][c] = __shfl_sync(0xffffffffu, sums[b], from);
+                for (int b = 0; b < NB; ++b) qc[nt][b][c] = qc[nt][b][c + 2] = __shfl_sync(0xffffffffu, sums[b], from);
                 const int ec = __shfl_sync(0xffffffffu, e, from);
                 // 2^24 of the codes and 2^-e of the row, in two steps (e reaches 126)
-                yscale[nt][c] = p.scale * 16777216.f * exp2_int(-ec);
+                yscale[nt][c] = p.scale == 0.f ? 1.f : fmaxf(fabsf(p.scale) * 16777216.f * exp2_int(-ec), 1.17549435e-38f);
                 const int rc = at.rt * R + nt * 8 + 2 * t + c;
                 const int pos = s.len - s.qlen + rc / p.group;
                 hi[nt][c] = p.causal ? pos : s.len - 1;
@@ -411,14 +427,6 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
             const uint32_t kb = ring + st * C::kStage, vb = kb + kTile * RB;
             const int key0 = (s.t0 + at.tile + i) * kTile;
             const uint32_t there = vmask[st];
-            // key of row r of the j-th 16: strides that keep the eight rows of
-            // a load on different banks
-            auto tau = [](int j, int r) {
-                const int gg = r & 7, up = r >> 3;
-                if (NB == 4) return 16 * j + 2 * gg + up;
-                if (NB == 8) return 16 * j + r;
-                return 4 * gg + 2 * j + up;
-            };
             // ---- S
             float y[2][NT][4];
 #pragma unroll
@@ -444,9 +452,9 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
                         const uint32_t e0 = c0 >> 8, e1 = c1 >> 8;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            float acc[4] = {qc[nt][b][0], qc[nt][b][1], qc[nt][b][0], qc[nt][b][1]};
-                            mma_f16(acc, c0 & 0x000f000fu, c1 & 0x000f000fu, c0 & 0x00f000f0u, c1 & 0x00f000f0u,
-                                    qb[nt][b][0], qb[nt][b][1]);
+                            float acc[4];
+                            mma_f16c(acc, c0 & 0x000f000fu, c1 & 0x000f000fu, c0 & 0x00f000f0u, c1 & 0x00f000f0u,
+                                     qb[nt][b][0], qb[nt][b][1], qc[nt][b]);
                             mma_f16(acc, e0 & 0x000f000fu, e1 & 0x000f000fu, e0 & 0x00f000f0u, e1 & 0x00f000f0u,
                                     qb[nt][b][2], qb[nt][b][3]);
 #pragma unroll
@@ -456,14 +464,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
                     }
                 }
             }
-            const bool edge = there != 0xffffffffu || key0 + kTile - 1 > all_hi || key0 < all_lo;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) y[j][nt][k] *= yscale[nt][k & 1];
-            if (edge) {
+            if (there != 0xffffffffu || key0 + kTile - 1 > all_hi || key0 < all_lo) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -475,32 +476,38 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
                             if (!ok) y[j][nt][k] = -INFINITY;
                         }
             }
-            // ---- value scales: pairs of keys 2t, 2t + 1 and 2t + 8, 2t + 9 of each 16
-            uint32_t dv[2][NB][2];
+            // ---- value scales, lane = key; a key that no row sees has 0
+            uint32_t dv[NB];
             uint32_t dm = 0;
+            {
+                const int key = key0 + lane;
+                const bool seen = key < s.len && key >= s.lo && ((there >> lane) & 1u);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int up = 0; up < 2; ++up) {
-                    const int ka = tau(j, 2 * t + 8 * up), kc = tau(j, 2 * t + 1 + 8 * up);
-                    uint32_t keep = 0xffffffffu;
-                    if (edge) {
-                        const bool a = key0 + ka < s.len && ((there >> ka) & 1u), c = key0 + kc < s.len && ((there >> kc) & 1u);
-                        keep = (a ? 0xffffu : 0u) | (c ? 0xffff0000u : 0u);
-                    }
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        const uint32_t x = lds_u16(vb + ka * RB + 18 * b), z = lds_u16(vb + kc * RB + 18 * b);
-                        dv[j][b][up] = (x | (z << 16)) & keep;
-                        dm = hmax2_u32(dm, dv[j][b][up] & 0x7fff7fffu);
-                    }
+                for (int b = 0; b < NB; ++b) {
+                    dv[b] = lds_u16(vb + lane * RB + 18 * b);
+                    if (!seen) dv[b] = 0;
+                    dm = max(dm, dv[b] & 0x7fffu);
                 }
-            dm = hmax2_u32(dm, __shfl_xor_sync(0xffffffffu, dm, 1));
-            dm = hmax2_u32(dm, __shfl_xor_sync(0xffffffffu, dm, 2));
-            const uint32_t dmx = max(dm & 0xffffu, dm >> 16);
+            }
+            const uint32_t dmx = __reduce_max_sync(0xffffffffu, dm);
+            if (dmx >= 0x7c00u) {
+                // a scale that is not finite: 0 in the product, and the rows that see its key become NaN
+                const unsigned who = __ballot_sync(0xffffffffu, dm >= 0x7c00u);
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    if ((dv[b] & 0x7c00u) == 0x7c00u) dv[b] = 0;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (((who >> tau(j, g + 8 * (k >> 1))) & 1u) && y[j][nt][k] != -INFINITY)
+                                l[nt][k & 1] = __int_as_float(0x7fc00000);
+            }
+            // ---- running maximum, value exponent
             int ne = static_cast<int>(dmx >> 10) - 15;
-            ne = ne < -14 ? -14 : (ne > 14 ? 14 : ne);
-            // ---- running maximum
+            ne = ne > 14 ? 14 : ne;
             bool grow = ne > ve;
             float mt[NT][2];
 #pragma unroll
@@ -511,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    mt[nt][c] = fmaxf(m[nt][c], v);
+                    mt[nt][c] = fmaxf(m[nt][c], v * yscale[nt][c]);
                     grow |= mt[nt][c] > m[nt][c];
                 }
             if (__any_sync(0xffffffffu, grow)) {
@@ -532,20 +539,28 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
                         }
                     }
             }
-            const uint32_t vs = static_cast<uint32_t>((15 - ve) << 10) * 0x10001u;   // 2^-ve
+            {
+                const uint32_t vs = static_cast<uint32_t>((15 - ve) << 10) * 0x10001u;   // 2^-ve
+#pragma unroll
+                for (int b = 0; b < NB; b += 2) {
+                    const uint32_t two = hmul2_u32(dv[b] | (dv[b + 1] << 16), vs);
+                    sts_u16(scale_at + 64 * b, two);
+                    sts_u16(scale_at + 64 * b + 64, two >> 16);
+                }
+            }
             // ---- P (2^13 P, binary16), transposed into B operand words
             uint32_t pb[2][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float mm[2];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) mm[c] = m[nt][c] == -INFINITY ? 0.f : 13.f - m[nt][c];
+                for (int c = 0; c < 2; ++c) mm[c] = m[nt][c] == -INFINITY ? 0.f : 13.f - m[nt][c];   // (all hidden: 2^-inf)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     float e[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        e[k] = ex2(y[j][nt][k] + mm[k & 1]);
+                        e[k] = ex2(fmaf(y[j][nt][k], yscale[nt][k & 1], mm[k & 1]));
                         l[nt][k & 1] += e[k];
                     }
                     pb[j][nt][0] = movm(pack_f16x2(e[0], e[1]));
@@ -553,6 +568,10 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
                 }
             }
             // ---- O
+            __syncwarp();
+            uint4 dq[NB];   // scales of the keys 2t, 2t + 1, 2t + 8, 2t + 9 of both 16s
+#pragma unroll
+            for (int b = 0; b < NB; ++b) dq[b] = lds128(scales + 64 * b + 16 * t);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const uint32_t ra = vb + tau(j, 2 * t) * RB, rb = vb + tau(j, 2 * t + 1) * RB;
@@ -560,17 +579,13 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     const uint32_t c = 18 * b + 2 + 2 * g;
-                    const uint32_t x = lds_u16(ra + c) | (lds_u16(rb + c) << 16);
-                    const uint32_t z = lds_u16(rc + c) | (lds_u16(rd + c) << 16);
-                    const uint32_t x8 = x >> 8, z8 = z >> 8;
-                    const uint32_t d0 = hmul2_u32(dv[j][b][0], vs), d1 = hmul2_u32(dv[j][b][1], vs);
+                    const uint32_t xa = lds_u16(ra + c), xb = lds_u16(rb + c), xc = lds_u16(rc + c), xd = lds_u16(rd + c);
+                    const uint32_t x = __byte_perm(xa, xb, 0x5410), x8 = __byte_perm(xa, xb, 0x6521);
+                    const uint32_t z = __byte_perm(xc, xd, 0x5410), z8 = __byte_perm(xc, xd, 0x6521);
+                    const uint32_t d0 = j ? dq[b].z : dq[b].x, d1 = j ? dq[b].w : dq[b].y;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        uint32_t b0 = hmul2_u32(pb[j][nt][0], d0), b1 = hmul2_u32(pb[j][nt][1], d1);
-                        if (edge) {   // a key this row does not see adds nothing, whatever its scale
-                            b0 &= half_mask(pb[j][nt][0]);
-                            b1 &= half_mask(pb[j][nt][1]);
-                        }
+                        const uint32_t b0 = hmul2_u32(pb[j][nt][0], d0), b1 = hmul2_u32(pb[j][nt][1], d1);
                         // rows g, g + 8: dims 2g, 2g + 1 of the block's first (then second) 16
                         mma_f16(o[2 * b][nt], x & 0x000f000fu, x8 & 0x000f000fu, z & 0x000f000fu, z8 & 0x000f000fu, b0, b1);
                         mma_f16(o[2 * b][nt], 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, b0, b1);
@@ -618,39 +633,34 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
                     o[k][nt][c + 2] *= fk;
                 }
             }
-        // warps 4..6 leave theirs, warps 0..3 add
-        auto row_at = [&](int w, int k, int nt, int c) {
-            return reinterpret_cast<float2*>(join + (w * R + nt * 8 + 2 * t + c) * C::DP + 32 * (k >> 1) + 16 * (k & 1) + 2 * g);
-        };
-        if (warp >= 4) {
-#pragma unroll
-            for (int k = 0; k < 2 * NB; ++k)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) *row_at(warp - 4, k, nt, c) = make_float2(o[k][nt][c], o[k][nt][c + 2]);
-        }
-        bar_sync(1, 32 * kWarps);
-        if (warp < 4) {
+        // warps 3..5 leave theirs, warps 0..2 add, warp 6 adds to the first
+        static_assert(kWarps == 7, "three buffers join seven warps");
+        auto leave = [&](int w, bool add) {
 #pragma unroll
             for (int k = 0; k < 2 * NB; ++k)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float2* q2 = row_at(warp, k, nt, c);
-                        const float2 v = warp + 4 < kWarps ? *q2 : make_float2(0.f, 0.f);
+                        float2* q2 = reinterpret_cast<float2*>(join + (w * R + nt * 8 + 2 * t + c) * C::DP + 32 * (k >> 1) +
+                                                               16 * (k & 1) + 2 * g);
+                        const float2 v = add ? *q2 : make_float2(0.f, 0.f);
                         *q2 = make_float2(v.x + o[k][nt][c], v.y + o[k][nt][c + 2]);
                     }
-        }
+        };
+        if (warp >= 3 && warp < 6) leave(warp - 3, false);
         bar_sync(1, 32 * kWarps);
-        // sum of the four buffers: the output, or this CTA's partial result
+        if (warp < 3) leave(warp, true);
+        bar_sync(1, 32 * kWarps);
+        if (warp == 6) leave(0, true);
+        bar_sync(1, 32 * kWarps);
+        // sum of the buffers: the output, or this CTA's partial result
         float* part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * C::kSlot;
         for (int i = tid; i < R * (D / 4); i += 32 * kWarps) {
             const int r = i / (D / 4), c4 = (i % (D / 4)) * 4;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < 3; ++w) {
                 const float4 x = *reinterpret_cast<const float4*>(join + (w * R + r) * C::DP + c4);
                 v.x += x.x;
                 v.y += x.y;
