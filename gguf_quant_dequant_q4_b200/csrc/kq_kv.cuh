@@ -49,6 +49,8 @@ struct AttnParams {
     const uint8_t* kp;
     const uint8_t* vp;
     int n_pages, page;
+    uint32_t page_mul;           // division by the page size: see page_of
+    int page_shift;
     const int32_t* table;
     int max_blocks;
     float scale;                 // times log2(e)
@@ -59,6 +61,14 @@ struct AttnParams {
     int32_t* err;
     int* status;
 };
+
+// Table place of a key (a multiple of 16): floor(n / d) of n = key / 8 < 2^27
+// and d = page / 8 as umulhi(n, m) >> k with 2^k < d <= 2^(k + 1) and m =
+// ceil(2^(32 + k) / d) < 2^32: m d exceeds 2^(32 + k) by less than d, and n d <=
+// 2^27 2^(k + 1) < 2^(32 + k), so the product's error stays below 1 / d.
+__device__ __forceinline__ int page_of(const AttnParams& p, int key) {
+    return static_cast<int>(__umulhi(static_cast<uint32_t>(key) >> 3, p.page_mul) >> p.page_shift);
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;

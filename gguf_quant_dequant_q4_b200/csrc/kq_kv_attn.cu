@@ -10,7 +10,7 @@
 //   S[key, row]  = sum over blocks of d(key, block) * ((code - 8) . q)   where
 //                  the -8 is the accumulator's start, -8 * sum of the block's q
 //   O[dim, row] += (code - 8)[dim, key] * (P d)[key, row]                 where
-//                  the -8 is one more MMA with a constant operand.
+//                  the -8 comes off at the end, as 8 sum P d in fp32.
 // q is scaled by a power of two per row (as every decode kernel of this
 // library), so only P and P * d are rounded, to binary16, each by at most
 // 2^-11 of its value: P is held as 2^13 * P and d is divided by a power of
@@ -23,7 +23,7 @@
 // a grid that fills the GPU once takes an equal run of it, whatever the
 // lengths (found on the device from the lengths; the host reads nothing).  In
 // a CTA one warp reads the block table and issues bulk copies of 16- or
-// 32-key runs into a ring of stages; seven warps take the tiles in turn, each
+// 32-key runs into a ring of stages; the other warps take the tiles in turn, each
 // with a maximum, sum and accumulator of its own, joined in shared memory at
 // the end of a segment.  A segment that spans CTAs leaves fp32 partial results
 // in the workspace, joined in list order by a second kernel: no atomics, the
@@ -36,9 +36,10 @@ namespace kq {
 namespace {
 
 constexpr int kTile = 32;        // keys of a tile
-constexpr int kWarps = 7;        // consumer warps (with the producer: 8, so that two CTAs have 128 registers a thread)
-constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kMinTiles = 8;     // least tiles of a CTA's share
+// P enters as 2^5 P, and a row's reference moves when its maximum is more than
+// 2^8 above it: P stays below 2^13, P * d below 2^15.
+constexpr float kPBias = 5.f, kLazy = 8.f;
 
 // A sequence's share of the work.
 struct Seq {
@@ -127,6 +128,9 @@ __device__ __forceinline__ int64_t share_of(int64_t total, int n_ctas) {
     return s < kMinTiles ? kMinTiles : s;
 }
 
+// x *= f in its own register (a rarely taken branch must not rename what the
+// other path would have to copy).
+__device__ __forceinline__ void mul_in_place(float& x, float f) { asm volatile("mul.f32 %0, %0, %1;" : "+f"(x) : "f"(f)); }
 __device__ __forceinline__ uint32_t movm(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -140,15 +144,6 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
 __device__ __forceinline__ void sts_u16(uint32_t a, uint32_t v) {
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(v)) : "memory");
 }
-// D = A B + C with C kept apart (fragments as mma_f16).
-__device__ __forceinline__ void mma_f16c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1, const float (&c)[4]) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %11, %12, %13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-}
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
 template <int NB, int NT>
@@ -158,10 +153,15 @@ struct Shape {
     static constexpr int RB = 18 * NB;                 // bytes of a row
     static constexpr int kStage = 2 * kTile * RB;      // keys, then values
     static constexpr bool two = NB * NT <= 4;          // two CTAs an SM
+    static constexpr int kWarps = two ? 7 : NB * NT <= 8 ? 11 : 7;   // consumer warps (and one producer)
+    static constexpr int kThreads = 32 * (kWarps + 1);
     static constexpr int DP = D + 4;                   // joined rows, padded (bank conflicts)
     static constexpr int kJoin = 3 * R * DP * 4;       // three buffers of fp32 rows
     static constexpr int kScale = 64 * NB;             // a warp's value scales of a tile, in operand order
-    static constexpr int kHead = 1024 + 2 * kWarps * R * 4 + kWarps * kScale;
+    static constexpr int kQ = NT * NB * 512;            // q as operand words, a 16-byte quad a lane
+    static constexpr int kStart = NT * NB * 64;         // the accumulators' start, a quad for every t
+    static constexpr int kRow = 3 * R * 4;              // of every row: y scale, last and first key seen
+    static constexpr int kHead = 1024 + 2 * kWarps * R * 4 + kWarps * kScale + kQ + kStart + kRow;
     static constexpr int kBudget = (two ? 113 : 226) * 1024;
     static constexpr int kFit = (kBudget - kHead - kJoin) / kStage;
     // A stage belongs to one consumer warp (NST a multiple of their number):
@@ -174,9 +174,9 @@ struct Shape {
 };
 
 template <int NB, int NT>
-__global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 2 : 1) attn_kernel(const AttnParams p) {
     using C = Shape<NB, NT>;
-    constexpr int R = C::R, RB = C::RB, NST = C::NST, D = C::D;
+    constexpr int R = C::R, RB = C::RB, NST = C::NST, D = C::D, kWarps = C::kWarps;
     static_assert(NST >= kWarps && NST % kWarps == 0, "stages of its own for every consumer warp");
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);
@@ -188,6 +188,11 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
     float* wm = reinterpret_cast<float*>(smem + 1024);   // [warp][R] maximum
     float* wl = wm + kWarps * R;                         // [warp][R] sum
     const uint32_t scales = smem_u32(smem) + 1024 + 2 * kWarps * R * 4 + (threadIdx.x >> 5) * C::kScale;
+    uint8_t* qmem = smem + 1024 + 2 * kWarps * R * 4 + kWarps * C::kScale;
+    const uint32_t qtab = smem_u32(qmem) + 16 * (threadIdx.x & 31), ctab = smem_u32(qmem) + C::kQ;
+    float* yrow = reinterpret_cast<float*>(qmem + C::kQ + C::kStart);
+    int* hirow = reinterpret_cast<int*>(yrow + R);
+    int* lorow = hirow + R;
     float* join = reinterpret_cast<float*>(smem + C::kHead);
     const uint32_t ring = smem_u32(smem) + C::kHead + C::kJoin;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -222,8 +227,8 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
     __syncthreads();
     Place at = *place;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (*abort_) return false;
         if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_) return false;
         if (!mbar_wait(bar, parity, p.status)) {
             *abort_ = 1;
             return false;
@@ -250,43 +255,59 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
         // Four lanes a tile (keys or values, first or second 16 keys), BT tiles
         // at a time: their table entries, waits and copies overlap.
         constexpr int BT = NST >= 16 ? 8 : 4;
-        uint32_t n = 0;   // tiles issued
+        uint32_t n = 0, phase = 0;   // next stage, its phase
+        const int64_t page_bytes = static_cast<int64_t>(p.n_kv) * p.page * RB;
         const int q = lane >> 2, kv = lane & 1, sl = (lane >> 1) & 1;
         Seq s = seq_of<R>(p, at.b);
         while (at.left > 0) {
             const int tiles = static_cast<int>(at.left < s.nt - at.tile ? at.left : s.nt - at.tile);
+            const uint8_t* src = (kv ? p.vp : p.kp) + static_cast<int64_t>(at.h) * p.page * RB;
+            const int32_t* row = p.table + static_cast<int64_t>(at.b) * p.max_blocks;
             // page of this lane's keys of tile i; -1: no visible key, -2: no such page
+            int rem = 0, page = -1;
             auto look = [&](int i) {
                 const int key = (s.t0 + at.tile + i) * kTile + 16 * sl;
-                if (q >= BT || i >= tiles || key >= s.len || key + 16 <= s.lo) return -1;
-                const int pg = p.table[static_cast<int64_t>(at.b) * p.max_blocks + key / p.page];
-                return pg < 0 || pg >= p.n_pages ? -2 : pg;
+                page = -1;
+                if (q < BT && i < tiles && key < s.len && key + 16 > s.lo) {
+                    const int blk = page_of(p, key);
+                    rem = key - blk * p.page;
+                    page = row[blk];
+                    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.n_pages)) page = -2;
+                }
             };
-            int next = look(q);
+            look(q);
             for (int i0 = 0; i0 < tiles; i0 += BT) {
-                const int pg = next, i = i0 + q;
-                next = look(i + BT);
+                const int pg = page, i = i0 + q;
+                const uint8_t* from = src + pg * page_bytes + rem * RB;
+                const bool run = sl ? rem >= 16 : rem + 32 <= p.page;   // the tile's keys are one run
+                look(i + BT);
                 if (pg == -2 && kv == 0 && p.err) atomicOr(p.err, KQ_DEV_BAD_RANGE);
-                const int key = (s.t0 + at.tile + i) * kTile + 16 * sl;
-                const int64_t off = ((static_cast<int64_t>(pg) * p.n_kv + at.h) * p.page + key % p.page) * RB;
-                const unsigned in = __ballot_sync(0xffffffffu, pg >= 0) >> (lane & 28);
-                const int64_t off0 = __shfl_sync(0xffffffffu, off, lane & 29), off1 = __shfl_sync(0xffffffffu, off, lane | 2);
-                const bool both = (in & 5u) == 5u && off1 == off0 + 16 * RB;   // one run of 32 keys
-                const uint32_t st = (n + q) % NST;
+                const unsigned in = (__ballot_sync(0xffffffffu, pg >= 0) >> (lane & 28)) & 15u;
+                uint32_t st = n + q;
+                uint32_t par = phase ^ 1;
+                if (st >= NST) {
+                    st -= NST;
+                    par ^= 1;
+                }
                 bool ok = q < BT && i < tiles;
                 if (ok && (lane & 3) == 0) {
-                    ok = wait(&empty[st], (((n + q) / NST) & 1) ^ 1);
+                    ok = wait(&empty[st], par);
                     if (ok) {
                         vmask[st] = ((in & 1u) ? 0xffffu : 0u) | ((in & 4u) ? 0xffff0000u : 0u);
-                        mbar_arrive_expect_tx(&full[st], ((in & 1u) + ((in >> 2) & 1u)) * 32 * RB);
+                        mbar_arrive_expect_tx(&full[st], __popc(in) * 16 * RB);
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, lane & 28);
+                const bool both = in == 15u && run;
                 if (ok && pg >= 0 && !(both && sl)) {
                     uint8_t* d = smem + C::kHead + C::kJoin + st * C::kStage + (kv * kTile + sl * 16) * RB;
-                    bulk_g2s(d, (kv ? p.vp : p.kp) + off, both ? 32 * RB : 16 * RB, &full[st]);
+                    bulk_g2s(d, from, both ? 32 * RB : 16 * RB, &full[st]);
                 }
                 n += tiles - i0 < BT ? tiles - i0 : BT;
+                if (n >= NST) {
+                    n -= NST;
+                    phase ^= 1;
+                }
             }
             at.left -= tiles;
             if (at.left > 0) advance(s);
@@ -317,20 +338,17 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
 #pragma unroll
         for (int r = 0; r < 16; ++r)
             if (tau(j, r) == lane) scale_at += 16 * ((r & 7) >> 1) + 8 * j + 4 * (r >> 3) + 2 * (r & 1);
-    uint32_t n0 = 0;             // tiles before this segment
+    int first = warp;            // this warp's first tile of the segment
+    uint32_t stage = warp, phase = 0;
     Seq s = seq_of<R>(p, at.b);
     int slot = 0;                // partial slot: 0 while in the share's first segment
     while (at.left > 0) {
         const int tiles = static_cast<int>(at.left < s.nt - at.tile ? at.left : s.nt - at.tile);
         const bool whole = tiles == s.nt;
         const int rows = s.qlen * p.group - at.rt * R;   // rows of this tile that exist (may exceed R)
-        // ---- q: operand words and the accumulators' start
-        uint32_t qb[NT][NB][4];
-        float qc[NT][NB][4];
-        float yscale[NT][2];
-        int hi[NT][2], lo[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        // ---- q: operand words and the accumulators' start, 8 rows a warp
+        if (warp < NT) {
+            const int nt = warp;
             const int r = nt * 8 + g;
             const int rr = at.rt * R + r, i = rr / p.group;
             const bool there = r < rows;
@@ -362,7 +380,6 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
             const int e = xscale_exp(mx, 13);
             // the scale's sign goes into q, so that yscale > 0; scale 0: q = 0
             const float up = p.scale == 0.f ? 0.f : copysignf(exp2_int(e), p.scale);
-            float sums[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 float v[8];      // lo of bytes 0..3, hi of bytes 0..3
@@ -374,31 +391,36 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
                     v[4 * hf + 3] = bf16hi_to_f32(w[b][hf].y) * up;
                 }
                 // high nibbles enter the MMA as 16 * code
-                qb[nt][b][0] = pack_f16x2(v[0], v[2]);
-                qb[nt][b][1] = pack_f16x2(v[4] * 0.0625f, v[6] * 0.0625f);
-                qb[nt][b][2] = pack_f16x2(v[1], v[3]);
-                qb[nt][b][3] = pack_f16x2(v[5] * 0.0625f, v[7] * 0.0625f);
+                const uint32_t w4[4] = {pack_f16x2(v[0], v[2]), pack_f16x2(v[4] * 0.0625f, v[6] * 0.0625f),
+                                        pack_f16x2(v[1], v[3]), pack_f16x2(v[5] * 0.0625f, v[7] * 0.0625f)};
+                *reinterpret_cast<uint4*>(qmem + (nt * NB + b) * 512 + 16 * lane) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
                 float a = 0.f;   // of the rounded operands
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    a += (f16lo_to_f32(qb[nt][b][k]) + f16hi_to_f32(qb[nt][b][k])) * (k & 1 ? 16.f : 1.f);
+                for (int k = 0; k < 4; ++k) a += (f16lo_to_f32(w4[k]) + f16hi_to_f32(w4[k])) * (k & 1 ? 16.f : 1.f);
                 a += __shfl_xor_sync(0xffffffffu, a, 1);
                 a += __shfl_xor_sync(0xffffffffu, a, 2);
-                sums[b] = a * (-8.f / 16777216.f);
+                a *= -8.f / 16777216.f;
+                // row g is column g & 1 of t = g / 2, in both of its rows
+                if (t == 0) {
+                    float* st = reinterpret_cast<float*>(qmem + C::kQ + (nt * NB + b) * 64 + 16 * (g >> 1)) + (g & 1);
+                    st[0] = a;
+                    st[2] = a;
+                }
             }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int from = 4 * (2 * t + c);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) qc[nt][b][c] = qc[nt][b][c + 2] = __shfl_sync(0xffffffffu, sums[b], from);
-                const int ec = __shfl_sync(0xffffffffu, e, from);
+            if (t == 0) {
                 // 2^24 of the codes and 2^-e of the row, in two steps (e reaches 126)
-                yscale[nt][c] = p.scale == 0.f ? 1.f : fmaxf(fabsf(p.scale) * 16777216.f * exp2_int(-ec), 1.17549435e-38f);
-                const int rc = at.rt * R + nt * 8 + 2 * t + c;
-                const int pos = s.len - s.qlen + rc / p.group;
-                hi[nt][c] = p.causal ? pos : s.len - 1;
-                lo[nt][c] = p.window > 0 ? pos - p.window + 1 : 0;
+                yrow[r] = p.scale == 0.f ? 1.f : fmaxf(fabsf(p.scale) * 16777216.f * exp2_int(-e), 1.17549435e-38f);
+                const int pos = s.len - s.qlen + i;
+                hirow[r] = p.causal ? min(pos, s.len - 1) : s.len - 1;
+                lorow[r] = p.window > 0 ? pos - p.window + 1 : 0;
             }
+        }
+        bar_sync(1, 32 * kWarps);
+        float yscale[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            yscale[nt][0] = yrow[nt * 8 + 2 * t];
+            yscale[nt][1] = yrow[nt * 8 + 2 * t + 1];
         }
         // keys that every row of the segment sees
         const int pos0 = s.len - s.qlen + (at.rt * R) / p.group;
@@ -408,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
         const int all_lo = p.window > 0 ? pos1 - p.window + 1 : 0;
 
         float o[2 * NB][NT][4];
+        float pd[NT][NB];        // this lane's part of sum P d of row g
         float m[NT][2], l[NT][2];
         int ve = -14;            // exponent of the value scale
 #pragma unroll
@@ -416,29 +439,42 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
             for (int i = 0; i < 2 * NB; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[i][nt][k] = 0.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) pd[nt][b] = 0.f;
             m[nt][0] = m[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
         }
 
         // this warp's tiles: list positions n with n % kWarps == warp
-        for (int i = static_cast<int>((warp + kWarps - n0 % kWarps) % kWarps); i < tiles; i += kWarps) {
-            const uint32_t n = n0 + i, st = n % NST;
-            if (!__all_sync(0xffffffffu, wait(&full[st], (n / NST) & 1))) continue;
+        int i = first;
+        for (; i < tiles; i += kWarps) {
+            const uint32_t st = stage;
+            const bool ok = __all_sync(0xffffffffu, wait(&full[st], phase));
+            stage += kWarps;
+            if (stage >= NST) {
+                stage -= NST;
+                phase ^= 1;
+            }
+            if (!ok) continue;
             const uint32_t kb = ring + st * C::kStage, vb = kb + kTile * RB;
             const int key0 = (s.t0 + at.tile + i) * kTile;
             const uint32_t there = vmask[st];
             // ---- S
             float y[2][NT][4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t r0 = kb + tau(j, g) * RB, r1 = kb + tau(j, g + 8) * RB;
+            for (int bp = 0; bp < NB / 2; ++bp) {
+                uint4 qw[2][NT];
 #pragma unroll
-                for (int bp = 0; bp < NB / 2; ++bp) {
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) qw[hf][nt] = lds128(qtab + (nt * NB + 2 * bp + hf) * 512);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
                     uint32_t cw[2][2];   // [block of the pair][row]
                     float d[2][2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const uint32_t a = (r ? r1 : r0) + 36 * bp;
+                        const uint32_t a = kb + tau(j, g + 8 * r) * RB + 36 * bp;
                         const uint32_t w0 = lds32(a), w4 = lds32(a + 16), wx = lds32(a + 4 + 4 * t);
                         cw[1][r] = lds32(a + 20 + 4 * t);
                         cw[0][r] = __byte_perm(w0, wx, t == 3 ? 0x5432 : 0x7654);
@@ -452,11 +488,13 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
                         const uint32_t e0 = c0 >> 8, e1 = c1 >> 8;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            float acc[4];
-                            mma_f16c(acc, c0 & 0x000f000fu, c1 & 0x000f000fu, c0 & 0x00f000f0u, c1 & 0x00f000f0u,
-                                     qb[nt][b][0], qb[nt][b][1], qc[nt][b]);
+                            const uint4 st4 = lds128(ctab + (nt * NB + b) * 64 + 16 * t);
+                            float acc[4] = {__uint_as_float(st4.x), __uint_as_float(st4.y), __uint_as_float(st4.z),
+                                            __uint_as_float(st4.w)};
+                            mma_f16(acc, c0 & 0x000f000fu, c1 & 0x000f000fu, c0 & 0x00f000f0u, c1 & 0x00f000f0u,
+                                    qw[hf][nt].x, qw[hf][nt].y);
                             mma_f16(acc, e0 & 0x000f000fu, e1 & 0x000f000fu, e0 & 0x00f000f0u, e1 & 0x00f000f0u,
-                                    qb[nt][b][2], qb[nt][b][3]);
+                                    qw[hf][nt].z, qw[hf][nt].w);
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 y[j][nt][k] = b == 0 ? d[hf][k >> 1] * acc[k] : fmaf(d[hf][k >> 1], acc[k], y[j][nt][k]);
@@ -464,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
                     }
                 }
             }
-            if (there != 0xffffffffu || key0 + kTile - 1 > all_hi || key0 < all_lo) {
+            const bool edge = there != 0xffffffffu || key0 + kTile - 1 > all_hi || key0 < all_lo;
+            if (edge) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -472,7 +511,8 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int tk = tau(j, g + 8 * (k >> 1)), key = key0 + tk;
-                            const bool ok = key < s.len && key <= hi[nt][k & 1] && key >= lo[nt][k & 1] && ((there >> tk) & 1u);
+                            const int r = nt * 8 + 2 * t + (k & 1);
+                            const bool ok = key <= hirow[r] && key >= lorow[r] && ((there >> tk) & 1u);
                             if (!ok) y[j][nt][k] = -INFINITY;
                         }
             }
@@ -480,14 +520,16 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
             uint32_t dv[NB];
             uint32_t dm = 0;
             {
-                const int key = key0 + lane;
-                const bool seen = key < s.len && key >= s.lo && ((there >> lane) & 1u);
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    dv[b] = lds_u16(vb + lane * RB + 18 * b);
-                    if (!seen) dv[b] = 0;
-                    dm = max(dm, dv[b] & 0x7fffu);
+                for (int b = 0; b < NB; ++b) dv[b] = lds_u16(vb + lane * RB + 18 * b);
+                if (edge) {
+                    const int key = key0 + lane;
+                    const bool seen = key < s.len && key >= s.lo && ((there >> lane) & 1u);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) dv[b] = seen ? dv[b] : 0;
                 }
+#pragma unroll
+                for (int b = 0; b < NB; ++b) dm = max(dm, dv[b] & 0x7fffu);
             }
             const uint32_t dmx = __reduce_max_sync(0xffffffffu, dm);
             if (dmx >= 0x7c00u) {
@@ -508,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
             // ---- running maximum, value exponent
             int ne = static_cast<int>(dmx >> 10) - 15;
             ne = ne > 14 ? 14 : ne;
-            bool grow = ne > ve;
+            bool grow = ne > ve + 1;
             float mt[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -519,25 +561,32 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
                     mt[nt][c] = fmaxf(m[nt][c], v * yscale[nt][c]);
-                    grow |= mt[nt][c] > m[nt][c];
+                    grow |= mt[nt][c] > m[nt][c] + kLazy;
                 }
             if (__any_sync(0xffffffffu, grow)) {
                 const int e = ne > ve ? ne : ve;
                 const float fe = exp2_int(ve - e);
                 ve = e;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
+                    float f[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float f = m[nt][c] == mt[nt][c] ? 1.f : ex2(m[nt][c] - mt[nt][c]);
+                        f[c] = m[nt][c] == mt[nt][c] ? 1.f : ex2(m[nt][c] - mt[nt][c]);
                         m[nt][c] = mt[nt][c];
-                        l[nt][c] *= f;
+                        mul_in_place(l[nt][c], f[c]);
+                        f[c] *= fe;
 #pragma unroll
                         for (int k = 0; k < 2 * NB; ++k) {
-                            o[k][nt][c] *= f * fe;
-                            o[k][nt][c + 2] *= f * fe;
+                            mul_in_place(o[k][nt][c], f[c]);
+                            mul_in_place(o[k][nt][c + 2], f[c]);
                         }
                     }
+                    // row g is column g & 1 of t = g / 2
+                    const float fa = __shfl_sync(0xffffffffu, f[0], g >> 1), fb = __shfl_sync(0xffffffffu, f[1], g >> 1);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) mul_in_place(pd[nt][b], (g & 1) ? fb : fa);
+                }
             }
             {
                 const uint32_t vs = static_cast<uint32_t>((15 - ve) << 10) * 0x10001u;   // 2^-ve
@@ -548,13 +597,13 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
                     sts_u16(scale_at + 64 * b + 64, two >> 16);
                 }
             }
-            // ---- P (2^13 P, binary16), transposed into B operand words
+            // ---- P (2^5 P, binary16), transposed into B operand words
             uint32_t pb[2][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float mm[2];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) mm[c] = m[nt][c] == -INFINITY ? 0.f : 13.f - m[nt][c];   // (all hidden: 2^-inf)
+                for (int c = 0; c < 2; ++c) mm[c] = m[nt][c] == -INFINITY ? 0.f : kPBias - m[nt][c];   // (all hidden: 2^-inf)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     float e[4];
@@ -580,23 +629,44 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
                 for (int b = 0; b < NB; ++b) {
                     const uint32_t c = 18 * b + 2 + 2 * g;
                     const uint32_t xa = lds_u16(ra + c), xb = lds_u16(rb + c), xc = lds_u16(rc + c), xd = lds_u16(rd + c);
-                    const uint32_t x = __byte_perm(xa, xb, 0x5410), x8 = __byte_perm(xa, xb, 0x6521);
-                    const uint32_t z = __byte_perm(xc, xd, 0x5410), z8 = __byte_perm(xc, xd, 0x6521);
+                    // whole bytes (low code + 16 * high code) of both keys, and the low codes
+                    const uint32_t x0 = __byte_perm(xa, xb, 0x6420), x1 = __byte_perm(xa, xb, 0x6521);
+                    const uint32_t z0 = __byte_perm(xc, xd, 0x6420), z1 = __byte_perm(xc, xd, 0x6521);
                     const uint32_t d0 = j ? dq[b].z : dq[b].x, d1 = j ? dq[b].w : dq[b].y;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const uint32_t b0 = hmul2_u32(pb[j][nt][0], d0), b1 = hmul2_u32(pb[j][nt][1], d1);
                         // rows g, g + 8: dims 2g, 2g + 1 of the block's first (then second) 16
-                        mma_f16(o[2 * b][nt], x & 0x000f000fu, x8 & 0x000f000fu, z & 0x000f000fu, z8 & 0x000f000fu, b0, b1);
-                        mma_f16(o[2 * b][nt], 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, b0, b1);
-                        mma_f16(o[2 * b + 1][nt], x & 0x00f000f0u, x8 & 0x00f000f0u, z & 0x00f000f0u, z8 & 0x00f000f0u, b0, b1);
-                        mma_f16(o[2 * b + 1][nt], 0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u, b0, b1);
+                        mma_f16(o[2 * b][nt], x0 & 0x000f000fu, x1 & 0x000f000fu, z0 & 0x000f000fu, z1 & 0x000f000fu, b0, b1);
+                        mma_f16(o[2 * b + 1][nt], x0, x1, z0, z1, b0, b1);
+                        pd[nt][b] = add_f16hi(b1, add_f16lo(b1, add_f16hi(b0, add_f16lo(b0, pd[nt][b]))));
                     }
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
         }
+
+        first = i - tiles;
+        // high codes (times 16) out of the bytes, and the codes' offset, 8 sum
+        // P d, out of both
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float v = pd[nt][b];
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                v *= -8.f / 16777216.f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float x = __shfl_sync(0xffffffffu, v, 4 * (2 * t + c));
+                    o[2 * b + 1][nt][c] = fmaf(x, 16.f, o[2 * b + 1][nt][c] - o[2 * b][nt][c]);
+                    o[2 * b + 1][nt][c + 2] = fmaf(x, 16.f, o[2 * b + 1][nt][c + 2] - o[2 * b][nt][c + 2]);
+                    o[2 * b][nt][c] += x;
+                    o[2 * b][nt][c + 2] += x;
+                }
+            }
 
         // ---- join the warps
 #pragma unroll
@@ -633,8 +703,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
                     o[k][nt][c + 2] *= fk;
                 }
             }
-        // warps 3..5 leave theirs, warps 0..2 add, warp 6 adds to the first
-        static_assert(kWarps == 7, "three buffers join seven warps");
+        // three warps at a time leave or add theirs
         auto leave = [&](int w, bool add) {
 #pragma unroll
             for (int k = 0; k < 2 * NB; ++k)
@@ -648,12 +717,10 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
                         *q2 = make_float2(v.x + o[k][nt][c], v.y + o[k][nt][c + 2]);
                     }
         };
-        if (warp >= 3 && warp < 6) leave(warp - 3, false);
-        bar_sync(1, 32 * kWarps);
-        if (warp < 3) leave(warp, true);
-        bar_sync(1, 32 * kWarps);
-        if (warp == 6) leave(0, true);
-        bar_sync(1, 32 * kWarps);
+        for (int w = 0; w < kWarps; w += 3) {
+            if (warp >= w && warp < w + 3) leave(warp - w, w != 0);
+            bar_sync(1, 32 * kWarps);
+        }
         // sum of the buffers: the output, or this CTA's partial result
         float* part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * C::kSlot;
         for (int i = tid; i < R * (D / 4); i += 32 * kWarps) {
@@ -695,7 +762,6 @@ __global__ void __launch_bounds__(kThreads, Shape<NB, NT>::two ? 2 : 1) attn_ker
             }
         }
         bar_sync(1, 32 * kWarps);   // join, wm and wl are free again
-        n0 += tiles;
         at.left -= tiles;
         slot = 1;
         if (at.left > 0) advance(s);
@@ -775,7 +841,7 @@ int launch_of(AttnParams p, cudaStream_t s) {
         if (rc) return rc;
         if (dev < 64) ready[dev] = true;
     }
-    rc = launch_pdl(attn_kernel<NB, NT>, dim3(static_cast<unsigned>(p.n_ctas)), kThreads, C::kSmem, s, p);
+    rc = launch_pdl(attn_kernel<NB, NT>, dim3(static_cast<unsigned>(p.n_ctas)), C::kThreads, C::kSmem, s, p);
     if (rc) return rc;
     return launch_pdl(attn_join_kernel<NB, NT>, dim3(static_cast<unsigned>(p.n_ctas - 1), NB / 2), 128, 0, s, p);
 }
@@ -815,6 +881,10 @@ int launch_kv_attention(const KvAttention& a, cudaStream_t s) {
     p.vp = static_cast<const uint8_t*>(a.v_pool);
     p.n_pages = static_cast<int>(a.n_pages);
     p.page = a.page_size;
+    const uint64_t d = static_cast<uint64_t>(a.page_size) / 8;
+    p.page_shift = 0;
+    while ((uint64_t(2) << p.page_shift) < d) ++p.page_shift;
+    p.page_mul = static_cast<uint32_t>(((uint64_t(1) << (32 + p.page_shift)) + d - 1) / d);
     p.table = a.block_table;
     p.max_blocks = static_cast<int>(a.max_blocks);
     p.scale = a.scale * kLog2e;
