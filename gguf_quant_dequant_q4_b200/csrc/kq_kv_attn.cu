@@ -36,7 +36,11 @@ namespace kq {
 namespace {
 
 constexpr int kTile = 32;        // keys of a tile
-constexpr int kMinTiles = 8;     // least tiles of a CTA's share
+// A segment counts as its tiles and kSegCost more in the list: its queries,
+// first copies and join take about as long as that many tiles.  A CTA whose
+// part of a segment is within these has nothing to do there.
+constexpr int kSegCost = 20;
+constexpr int kMinShare = kSegCost + 7;   // least units of a CTA's share: a tile a warp
 // P enters as 2^5 P, and a row's reference moves when its maximum is more than
 // 2^8 above it: P stays below 2^13, P * d below 2^15.
 constexpr float kPBias = 5.f, kLazy = 8.f;
@@ -75,14 +79,27 @@ __device__ __forceinline__ Seq seq_of(const AttnParams& p, int b) {
     return s;
 }
 __device__ __forceinline__ int64_t units_of(const AttnParams& p, const Seq& s) {
-    return static_cast<int64_t>(s.nt) * s.rt * p.n_kv;
+    return static_cast<int64_t>(s.nt + kSegCost) * s.rt * p.n_kv;
 }
 
-// A place in the list: sequence, key head, row tile and tile.
+// A place in the list: sequence, key head, row tile and unit of the segment.
 struct Place {
-    int b, h, rt, tile;
+    int b, h, rt, unit;
     int64_t left;                // units of the CTA's share from here on
 };
+// The share's part of the segment at a place: units, and tiles [t0, t0 + n).
+struct Part {
+    int units, t0, n;
+};
+__device__ __forceinline__ Part part_of(const Place& at, const Seq& s) {
+    const int seg = s.nt + kSegCost;
+    Part r;
+    r.units = static_cast<int>(at.left < seg - at.unit ? at.left : seg - at.unit);
+    r.t0 = at.unit > kSegCost ? at.unit - kSegCost : 0;
+    const int end = at.unit + r.units - kSegCost;
+    r.n = end > r.t0 ? end - r.t0 : 0;
+    return r;
+}
 
 // Whole list length and the place of the unit at `share * blockIdx`, by the
 // threads of warp 0 .. all; results through shared memory.
@@ -125,7 +142,7 @@ __device__ __forceinline__ int list_find(const AttnParams& p, int64_t u, int64_t
 }
 __device__ __forceinline__ int64_t share_of(int64_t total, int n_ctas) {
     const int64_t s = (total + n_ctas - 1) / n_ctas;
-    return s < kMinTiles ? kMinTiles : s;
+    return s < kMinShare ? kMinShare : s;
 }
 
 // x *= f in its own register (a rarely taken branch must not rename what the
@@ -215,12 +232,12 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
         int64_t before;
         const int b = list_find<R>(p, u0, before);
         const Seq s = seq_of<R>(p, b);
-        const int64_t off = u0 - before, seg = off / s.nt;
+        const int64_t off = u0 - before, seg = off / (s.nt + kSegCost);
         if (lane == 0) {
             place->b = b;
             place->h = static_cast<int>(seg / s.rt);
             place->rt = static_cast<int>(seg % s.rt);
-            place->tile = static_cast<int>(off - seg * s.nt);
+            place->unit = static_cast<int>(off - seg * (s.nt + kSegCost));
             place->left = total - u0 < share ? total - u0 : share;
         }
     }
@@ -237,7 +254,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
     };
     // next segment of the list
     auto advance = [&](Seq& s) {
-        at.tile = 0;
+        at.unit = 0;
         if (++at.rt == s.rt) {
             at.rt = 0;
             if (++at.h == p.n_kv) {
@@ -260,13 +277,14 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
         const int q = lane >> 2, kv = lane & 1, sl = (lane >> 1) & 1;
         Seq s = seq_of<R>(p, at.b);
         while (at.left > 0) {
-            const int tiles = static_cast<int>(at.left < s.nt - at.tile ? at.left : s.nt - at.tile);
+            const Part part = part_of(at, s);
+            const int tiles = part.n, tile0 = s.t0 + part.t0;
             const uint8_t* src = (kv ? p.vp : p.kp) + static_cast<int64_t>(at.h) * p.page * RB;
             const int32_t* row = p.table + static_cast<int64_t>(at.b) * p.max_blocks;
             // page of this lane's keys of tile i; -1: no visible key, -2: no such page
             int rem = 0, page = -1;
             auto look = [&](int i) {
-                const int key = (s.t0 + at.tile + i) * kTile + 16 * sl;
+                const int key = (tile0 + i) * kTile + 16 * sl;
                 page = -1;
                 if (q < BT && i < tiles && key < s.len && key + 16 > s.lo) {
                     const int blk = page_of(p, key);
@@ -309,7 +327,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
                     phase ^= 1;
                 }
             }
-            at.left -= tiles;
+            at.left -= part.units;
             if (at.left > 0) advance(s);
         }
         if (*abort_) {
@@ -342,13 +360,22 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
     uint32_t stage = warp, phase = 0;
     Seq s = seq_of<R>(p, at.b);
     int slot = 0;                // partial slot: 0 while in the share's first segment
-    while (at.left > 0) {
-        const int tiles = static_cast<int>(at.left < s.nt - at.tile ? at.left : s.nt - at.tile);
-        const bool whole = tiles == s.nt;
-        const int rows = s.qlen * p.group - at.rt * R;   // rows of this tile that exist (may exceed R)
-        // ---- q: operand words and the accumulators' start, 8 rows a warp
+    Part pt{};
+    // the next part of the share that has tiles
+    auto settle = [&]() {
+        while (at.left > 0) {
+            pt = part_of(at, s);
+            if (pt.n > 0) return true;
+            at.left -= pt.units;
+            slot = 1;
+            if (at.left > 0) advance(s);
+        }
+        return false;
+    };
+    // q of the segment as operand words, and the accumulators' start, 8 rows a warp
+    auto prepare = [&]() {
         if (warp < NT) {
-            const int nt = warp;
+            const int nt = warp, rows = s.qlen * p.group - at.rt * R;
             const int r = nt * 8 + g;
             const int rr = at.rt * R + r, i = rr / p.group;
             const bool there = r < rows;
@@ -415,7 +442,14 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
                 lorow[r] = p.window > 0 ? pos - p.window + 1 : 0;
             }
         }
-        bar_sync(1, 32 * kWarps);
+    };
+    bool go = settle();
+    if (go) prepare();
+    bar_sync(1, 32 * kWarps);
+    while (go) {
+        const int tiles = pt.n, tile0 = s.t0 + pt.t0;
+        const bool whole = tiles == s.nt;
+        const int rows = s.qlen * p.group - at.rt * R;   // rows of this tile that exist (may exceed R)
         float yscale[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -457,7 +491,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
             }
             if (!ok) continue;
             const uint32_t kb = ring + st * C::kStage, vb = kb + kTile * RB;
-            const int key0 = (s.t0 + at.tile + i) * kTile;
+            const int key0 = (tile0 + i) * kTile;
             const uint32_t there = vmask[st];
             // ---- S
             float y[2][NT][4];
@@ -761,10 +795,12 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
                 }
             }
         }
-        bar_sync(1, 32 * kWarps);   // join, wm and wl are free again
-        at.left -= tiles;
+        at.left -= pt.units;
         slot = 1;
         if (at.left > 0) advance(s);
+        go = settle();
+        if (go) prepare();
+        bar_sync(1, 32 * kWarps);   // join, wm and wl are free again, q is there
     }
 }
 
@@ -793,13 +829,13 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p) {
     __syncthreads();
     const int b = static_cast<int>(found[0]);
     const Seq s = seq_of<R>(p, b);
-    const int64_t off = u - found[1], seg = off / s.nt;
-    const int64_t a = found[1] + seg * s.nt, e = a + s.nt;   // units of the segment
-    if (a == u || u - share > a) return;                     // not cut here, or cut before
+    const int64_t off = u - found[1], seg = off / (s.nt + kSegCost);
+    const int64_t a = found[1] + seg * (s.nt + kSegCost), t = a + kSegCost, e = t + s.nt;   // units: the segment, its tiles
+    if (t >= u || u - share > t) return;                     // its tiles are not cut here, or cut before
     const int h = static_cast<int>(seg / s.rt), rt = static_cast<int>(seg % s.rt);
-    const int c0 = static_cast<int>(a / share), c1 = static_cast<int>((e - 1) / share);
+    const int c0 = static_cast<int>(t / share), c1 = static_cast<int>((e - 1) / share);
     const int rows = s.qlen * p.group - rt * R;
-    auto slot = [&](int c) { return p.part + (static_cast<int64_t>(c) * 2 + (c > c0 || a == c * share ? 0 : 1)) * C::kSlot; };
+    auto slot = [&](int64_t c) { return p.part + (c * 2 + (c * share >= a ? 0 : 1)) * C::kSlot; };   // (0: the share's first segment)
     for (int i = threadIdx.x; i < R * 16; i += blockDim.x) {
         const int r = i / 16, c4 = static_cast<int>(blockIdx.y) * 64 + (i % 16) * 4;
         if (r >= rows) continue;
