@@ -43,6 +43,8 @@ struct AttnParams {
     uint16_t* out;               // [n_tokens, n_heads, D]
     int n_tokens;
     int n_heads, n_kv, group;
+    uint32_t group_mul;          // division by the group size: see group_of
+    int group_shift;
     const int32_t* cu;
     const int32_t* lens;
     int n_seqs;
@@ -62,6 +64,29 @@ struct AttnParams {
     int* status;
 };
 
+// Token of a row, floor(n / group) for n < 2^31: as page_of, with n 2^(k + 1) <
+// 2^(32 + k).
+__device__ __forceinline__ int group_of(const AttnParams& p, int n) {
+    return p.group == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), p.group_mul) >> p.group_shift);
+}
+// Bounded wait of a pipeline (all threads of a warp, or one): few instructions
+// while it lasts, so that warps that wait leave the issue slots to those that
+// work.  False once the limit has passed, or where another wait of the CTA has
+// run out before (*gone).
+__device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* gone, int* status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        if (*gone) return false;
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (global_ns() - t0 > kWaitLimitNs) break;
+    }
+    *gone = 1;
+    if (status) atomicOr(status, KQ_DEV_TIMEOUT);
+    return false;
+}
 // Table place of a key (a multiple of 16): floor(n / d) of n = key / 8 < 2^27
 // and d = page / 8 as umulhi(n, m) >> k with 2^k < d <= 2^(k + 1) and m =
 // ceil(2^(32 + k) / d) < 2^32: m d exceeds 2^(32 + k) by less than d, and n d <=

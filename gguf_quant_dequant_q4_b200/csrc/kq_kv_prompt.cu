@@ -33,9 +33,14 @@ namespace kq {
 namespace {
 
 constexpr int kRows = 256, kKeys = 128;
-constexpr int kThreads = 512;
+constexpr int kSoft = 16, kDec = 8;                 // warps: softmax, decoders
+constexpr int kMmaWarp = kSoft + kDec, kLoadWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kSoft + kDec + 4);   // seven warpgroups (two warps idle)
+// A segment counts as its tiles and kSegCost more in the list: its queries,
+// first tiles and output take about as long as that many tiles.
+constexpr int kSegCost = 4;
 constexpr int kRaw = 3;            // raw tiles in flight
-constexpr int kMinShare = 4;       // least tiles of a CTA's share
+constexpr int kMinShare = kSegCost + 3;   // least units of a CTA's share
 constexpr float kPBias = 7.f, kLazy = 8.f;
 
 // ---------------------------------------------------------------- PTX glue
@@ -93,6 +98,21 @@ __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* v) {
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
         KQ_I8(v, 0), KQ_I8(v, 8), KQ_I8(v, 16), KQ_I8(v, 24)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        : KQ_R8(v, 0), KQ_R8(v, 8)
+        : "r"(a)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(a),
+        KQ_I8(v, 0), KQ_I8(v, 8)
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -171,9 +191,9 @@ struct Span {
     int t0, n, lo;
 };
 __device__ __forceinline__ Span span_of(const AttnParams& p, const Seq& s, int rt) {
-    const int first = s.len - s.qlen + rt * kRows / p.group;
+    const int first = s.len - s.qlen + group_of(p, rt * kRows);
     const int end = min(rt * kRows + kRows, s.rows) - 1;
-    const int last = s.len - s.qlen + end / p.group;
+    const int last = s.len - s.qlen + group_of(p, end);
     int hi = p.causal ? last + 1 : s.len;     // one past the last key
     hi = hi < 0 ? 0 : (hi > s.len ? s.len : hi);
     int lo = p.window > 0 ? first - p.window + 1 : 0;
@@ -185,73 +205,121 @@ __device__ __forceinline__ Span span_of(const AttnParams& p, const Seq& s, int r
     r.n = n < 1 ? 1 : n;
     return r;
 }
-// Tiles of a sequence for one key head.
+// Units of a sequence for one key head.
 __device__ __forceinline__ int64_t tiles_of(const AttnParams& p, const Seq& s) {
     if (s.rows <= p.few) return 0;
     int64_t n = 0;
-    for (int rt = 0; rt * kRows < s.rows; ++rt) n += span_of(p, s, rt).n;
+    for (int rt = 0; rt * kRows < s.rows; ++rt) n += span_of(p, s, rt).n + kSegCost;
     return n;
 }
 
-__device__ __forceinline__ int64_t list_total(const AttnParams& p, unsigned long long* sum) {
-    if (threadIdx.x == 0) *sum = 0;
-    __syncthreads();
-    int64_t mine = 0;
-    for (int b = threadIdx.x; b < p.n_seqs; b += blockDim.x) mine += tiles_of(p, seq_of(p, b)) * p.n_kv;
-    if (mine) atomicAdd(sum, static_cast<unsigned long long>(mine));
-    __syncthreads();
-    return static_cast<int64_t>(*sum);
-}
-__device__ __forceinline__ int64_t share_of(int64_t total, int n_ctas) {
-    const int64_t s = (total + n_ctas - 1) / n_ctas;
-    return s < kMinShare ? kMinShare : s;
-}
-
-// A place in the list, and the units before its segment.
+// A place in the list (unit `unit` of a segment), and the units before the segment.
 struct Place {
-    int b, h, rt, tile;
+    int b, h, rt, unit;
     int64_t start;
 };
-// One warp: the place of unit u.
-__device__ __forceinline__ Place list_find(const AttnParams& p, int64_t u) {
-    const int lane = threadIdx.x & 31;
-    Place at{p.n_seqs, 0, 0, 0, 0};
-    int64_t base = 0;
-    for (int b0 = 0; b0 < p.n_seqs; b0 += 32) {
-        const int b = b0 + lane;
-        const int64_t per = b < p.n_seqs ? tiles_of(p, seq_of(p, b)) : 0;
-        const int64_t n = per * p.n_kv;
-        int64_t inc = n;
+// The share's part of the segment at a place: units, and tiles [t0, t0 + n) of
+// the row tile's span.
+struct Part {
+    int units, t0, n;
+};
+__device__ __forceinline__ Part part_of(const Place& at, const Span& sp, int left) {
+    Part r;
+    r.units = min(left, sp.n + kSegCost - at.unit);
+    r.t0 = max(at.unit - kSegCost, 0);
+    r.n = max(at.unit + r.units - kSegCost - r.t0, 0);
+    return r;
+}
+// The plan that one CTA leaves at the head of the work space: the list's
+// length, a CTA's share of it and where every share begins.
+struct Plan {
+    int64_t total, share;
+    Place at[1];
+};
+constexpr int kMostCtas = 255;
+constexpr int64_t kPlanBytes = 8192;
+static_assert(sizeof(Plan) + kMostCtas * sizeof(Place) <= kPlanBytes, "the plan's room");
+__device__ __forceinline__ Plan* plan_of(const AttnParams& p) { return reinterpret_cast<Plan*>(p.part); }
+__device__ __forceinline__ float* parts_of(const AttnParams& p) { return p.part + kPlanBytes / 4; }
+
+// One CTA of 256 threads: thread b's tiles of sequence b (a warp a sequence
+// where there are few, so that long prompts' row tiles are counted in
+// parallel), their running sums, and thread c's place of unit c * share.
+__global__ void __launch_bounds__(256) prompt_plan_kernel(const AttnParams p) {
+    __shared__ int64_t sums[256];
+    pdl_launch();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Plan* plan = plan_of(p);
+    // running sums of the tiles of sequences b0 .. b0 + 255, all heads
+    auto chunk = [&](int b0) {
+        if (p.n_seqs <= 32) {
+            if (tid < 256) sums[tid] = 0;
+            __syncthreads();
+            for (int b = warp; b < p.n_seqs; b += 8) {
+                const Seq s = seq_of(p, b);
+                int64_t n = 0;
+                if (s.rows > p.few)
+                    for (int rt = lane; static_cast<int64_t>(rt) * kRows < s.rows; rt += 32) n += span_of(p, s, rt).n + kSegCost;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
+                for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+                if (lane == 0) sums[b] = n * p.n_kv;
+            }
+        } else {
+            sums[tid] = b0 + tid < p.n_seqs ? tiles_of(p, seq_of(p, b0 + tid)) * p.n_kv : 0;
         }
-        const unsigned over = __ballot_sync(0xffffffffu, base + inc > u);
-        if (over) {
-            const int l = __ffs(over) - 1;
-            const int64_t before = base + __shfl_sync(0xffffffffu, inc - n, l);
-            const int64_t pr = __shfl_sync(0xffffffffu, per, l);
-            at.b = b0 + l;
-            at.h = static_cast<int>((u - before) / pr);
-            at.start = before + at.h * pr;
+        __syncthreads();
+        for (int o = 1; o < 256; o <<= 1) {
+            const int64_t v = tid >= o ? sums[tid - o] : 0;
+            __syncthreads();
+            sums[tid] += v;
+            __syncthreads();
+        }
+    };
+    int64_t total = 0;
+    for (int b0 = 0; b0 < p.n_seqs; b0 += 256) {
+        chunk(b0);
+        total += sums[255];
+        __syncthreads();
+    }
+    int64_t share = (total + p.n_ctas - 1) / p.n_ctas;
+    share = share < kMinShare ? kMinShare : share;
+    if (tid == 0) {
+        plan->total = total;
+        plan->share = share;
+    }
+    const int64_t u = share * tid;
+    int64_t base = 0;
+    for (int b0 = 0; b0 < p.n_seqs && base < total; b0 += 256) {
+        if (p.n_seqs > 256) chunk(b0);   // (one chunk is still there)
+        if (tid < p.n_ctas && u >= base && u < base + sums[255]) {
+            int lo = 0, hi = 255;
+            while (lo < hi) {            // the first whose running sum is past u
+                const int mid = (lo + hi) >> 1;
+                if (base + sums[mid] > u) hi = mid;
+                else lo = mid + 1;
+            }
+            Place at{b0 + lo, 0, 0, 0, 0};
+            const int64_t before = base + (lo ? sums[lo - 1] : 0), per = (base + sums[lo] - before) / p.n_kv;
+            at.h = static_cast<int>((u - before) / per);
+            at.start = before + at.h * per;
             const Seq s = seq_of(p, at.b);
             for (;;) {
-                const int k = span_of(p, s, at.rt).n;
+                const int k = span_of(p, s, at.rt).n + kSegCost;
                 if (u < at.start + k) break;
                 at.start += k;
                 ++at.rt;
             }
-            at.tile = static_cast<int>(u - at.start);
-            break;
+            at.unit = static_cast<int>(u - at.start);
+            plan->at[tid] = at;
         }
-        base += __shfl_sync(0xffffffffu, inc, 31);
+        base += sums[255];
+        __syncthreads();
     }
-    return at;
 }
 // The next segment of the list (there is one).
 __device__ __forceinline__ void advance(const AttnParams& p, Place& at, Seq& s) {
-    at.tile = 0;
+    at.unit = 0;
     ++at.rt;
     if (at.rt * kRows >= s.rows) {
         at.rt = 0;
@@ -272,61 +340,70 @@ struct Shape {
     static constexpr uint32_t kTileB = kKeys * D * 2;        // a key or value tile, a half of q
     static constexpr uint32_t kHalfB = kKeys * 128;          // its first 64 values
     static constexpr uint32_t kRawB = kKeys * RB;
-    static constexpr uint32_t kQ = 1024, kK = kQ + 2 * kTileB, kV = kK + 2 * kTileB, kRaw0 = kV + 2 * kTileB;
+    static constexpr uint32_t kEx = 1024;                    // exchange between the two sides of a row
+    static constexpr uint32_t kQ = kEx + 4 * kRows * 4, kK = kQ + 2 * kTileB, kV = kK + 2 * kTileB, kRaw0 = kV + 2 * kTileB;
     static constexpr uint32_t kSmem = kRaw0 + kRaw * kRawB + 1024;
     static constexpr int kSlot = kRows * D + 2 * kRows;      // floats of a partial result
+    // Tensor memory: S of both halves, O of both, and with 64-value heads P
+    // beside S, so that the next S is ready when a softmax ends; with 128 P
+    // takes the first half of its S.
+    static constexpr bool apart = NB == 2;
+    static constexpr uint32_t kO = 256, kP = apart ? 384 : 0, kPHalf = apart ? 64 : 128;
 };
 
 struct Bars {
     uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t s_full[2], p_full[2], o_full[2], q_full[2];
+    uint64_t s_full[2], s_free[2], p_full[4], o_full[2], q_full[2];
 };
 
 template <int NB>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p) {
     using C = Shape<NB>;
-    constexpr int D = C::D, RB = C::RB;
+    constexpr int D = C::D, RB = C::RB, HB = NB / 2;   // HB: blocks of one side
     static_assert(C::kSmem <= 232448, "shared memory of a CTA");
     extern __shared__ uint8_t smem_[];
     uint8_t* smem = smem_ + ((1024u - (smem_u32(smem_) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(smem);
     Bars& bar = *reinterpret_cast<Bars*>(smem);
     static_assert(sizeof(Bars) <= 512, "barriers");
-    uint32_t* tmask = reinterpret_cast<uint32_t*>(smem + 512);           // [16] runs of a tile that are there
+    volatile uint32_t* tmask = reinterpret_cast<volatile uint32_t*>(smem + 512);  // [16] runs of a tile that are there
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + 576);   // tensor memory, abort
-    unsigned long long* sum = reinterpret_cast<unsigned long long*>(smem + 592);
-    Place* place = reinterpret_cast<Place*>(smem + 608);
+    // [8] segments in turn: first and last key whose value scale is not finite
+    int* bad_lo = reinterpret_cast<int*>(smem + 640);
+    int* bad_hi = bad_lo + 8;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
         for (int i = 0; i < kRaw; ++i) {
             mbar_init(&bar.raw_full[i], 1);
-            mbar_init(&bar.raw_empty[i], 4);
+            mbar_init(&bar.raw_empty[i], kDec);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar.k_full[i], 4);
+            mbar_init(&bar.k_full[i], kDec);
             mbar_init(&bar.k_empty[i], 1);
-            mbar_init(&bar.v_full[i], 4);
+            mbar_init(&bar.v_full[i], kDec);
             mbar_init(&bar.v_empty[i], 1);
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 128);
+            mbar_init(&bar.s_free[i], 8);
+            mbar_init(&bar.p_full[i], 4);
+            mbar_init(&bar.p_full[i + 2], 4);
             mbar_init(&bar.o_full[i], 1);
-            mbar_init(&bar.q_full[i], 128);
+            mbar_init(&bar.q_full[i], 8);
+        }
+        for (int i = 0; i < 8; ++i) {
+            bad_lo[i] = 0x7fffffff;
+            bad_hi[i] = -1;
         }
         misc[1] = 0;
         fence_barrier_init();
     }
     pdl_launch();
     pdl_wait();
-    const int64_t total = list_total(p, sum);
-    const int64_t share = share_of(total, p.n_ctas);
+    const Plan* plan = plan_of(p);
+    const int64_t total = plan->total, share = plan->share;
     const int64_t u0 = share * blockIdx.x;
     if (u0 >= total) return;
-    if (warp == 0) {
-        const Place at = list_find(p, u0);
-        if (lane == 0) *place = at;
-    }
-    if (warp == 12) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sb + 576));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
@@ -334,31 +411,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
-    Place at = *place;
+    Place at = plan->at[blockIdx.x];
     Seq s = seq_of(p, at.b);
     int left = static_cast<int>(total - u0 < share ? total - u0 : share);
-    auto wait = [&](uint64_t* b, uint32_t parity) {
-        if (misc[1]) return false;
-        if (mbar_try_wait(b, parity)) return true;
-        if (!mbar_wait(b, parity, p.status)) {
-            misc[1] = 1;
-            return false;
-        }
-        return true;
-    };
+    auto wait = [&](uint64_t* b, uint32_t parity) { return kv_wait(b, parity, misc + 1, p.status); };
 
-    if (warp >= 12) {
+    if (warp >= kMmaWarp) {
         regs_dec<56>();
-        if (warp == 12) {
+        if (warp == kMmaWarp) {
             if (lane == 0) {
                 // -------------------------------------------- MMA issuer
                 constexpr uint32_t iqk = idesc_of(kKeys, false), ipv = idesc_of(D, true);
                 uint32_t n = 0;                          // tiles so far
                 uint32_t hn[2] = {0, 0}, hs[2] = {0, 0};   // tiles and segments of each half (the second may be idle)
-                while (left > 0) {
-                    const Span sp = span_of(p, s, at.rt);
-                    const int tiles = min(left, sp.n - at.tile);
-                    const int halves = s.rows - at.rt * kRows > 128 ? 2 : 1;
+                uint32_t hf[2] = {0, 0};                   // S given back
+                for (; left > 0;) {
+                    const Part pt = part_of(at, span_of(p, s, at.rt), left);
+                    const int tiles = pt.n;
+                    const int halves = tiles == 0 ? 0 : s.rows - at.rt * kRows > 128 ? 2 : 1;
                     bool ok = true;
                     for (int i = 0; i < halves; ++i) ok = ok && wait(&bar.q_full[i], hs[i] & 1);
                     auto qk = [&](int i, uint32_t m) {   // S of half i = q K^T, tile number m
@@ -371,72 +441,103 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                         }
                         tc_commit(&bar.s_full[i]);
                     };
-                    ok = ok && wait(&bar.k_full[n & 1], (n >> 1) & 1);
-                    if (ok) {
-                        tc_fence_after();
-                        for (int i = 0; i < halves; ++i) qk(i, n);
-                        tc_commit(&bar.k_empty[n & 1]);
+                    // O of half i += P V, tile number m, as the two sides of P come in
+                    auto pv = [&](int i, uint32_t m, bool first) {
+                        const uint64_t b = sw128_desc(sb + C::kV + (m & 1) * C::kTileB, C::kHalfB);
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            if (!wait(&bar.p_full[2 * i + z], hn[i] & 1)) return false;
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = 4 * z; k < 4 * z + 4; ++k)
+                                mma_ts(tmem + C::kO + i * D, tmem + C::kP + i * C::kPHalf + 8 * k, b + (k * 2048 >> 4), ipv,
+                                       !first || k != 0);
+                        }
+                        tc_commit(&bar.o_full[i]);
+                        return true;
+                    };
+                    if (tiles > 0) {
+                        ok = ok && wait(&bar.k_full[n & 1], (n >> 1) & 1);
+                        if (ok) {
+                            tc_fence_after();
+                            for (int i = 0; i < halves; ++i) qk(i, n);
+                            tc_commit(&bar.k_empty[n & 1]);
+                        }
                     }
                     for (int j = 0; j < tiles; ++j, ++n) {
                         const bool more = j + 1 < tiles;
-                        ok = ok && wait(&bar.v_full[n & 1], (n >> 1) & 1);
-                        for (int i = 0; i < halves; ++i) {
-                            ok = ok && wait(&bar.p_full[i], hn[i] & 1);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint64_t b = sw128_desc(sb + C::kV + (n & 1) * C::kTileB, C::kHalfB);
-#pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)
-                                mma_ts(tmem + 256 + i * D, tmem + i * 128 + 8 * k, b + (k * 2048 >> 4), ipv, j + k != 0);
+                        if constexpr (C::apart) {
                             if (more) {
-                                if (i == 0) ok = wait(&bar.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
-                                if (!ok) break;
-                                tc_fence_after();
-                                qk(i, n + 1);
-                            } else {
-                                tc_commit(&bar.o_full[i]);
+                                ok = ok && wait(&bar.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
+                                for (int i = 0; i < halves; ++i) {
+                                    ok = ok && wait(&bar.s_free[i], hf[i] & 1);
+                                    if (!ok) break;
+                                    ++hf[i];
+                                    tc_fence_after();
+                                    qk(i, n + 1);
+                                }
+                                if (ok) tc_commit(&bar.k_empty[(n + 1) & 1]);
                             }
                         }
+                        ok = ok && wait(&bar.v_full[n & 1], (n >> 1) & 1);
+                        for (int i = 0; i < halves; ++i) {
+                            ok = ok && pv(i, n, j == 0);
+                            if constexpr (!C::apart) {
+                                // S shares its room with P: after P V in the same queue
+                                if (more) {
+                                    if (i == 0) ok = ok && wait(&bar.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
+                                    if (ok) {
+                                        tc_fence_after();
+                                        qk(i, n + 1);
+                                    }
+                                }
+                            }
+                            if (!ok) break;
+                            ++hn[i];
+                        }
                         if (!ok) break;
-                        for (int i = 0; i < halves; ++i) ++hn[i];
-                        if (more) tc_commit(&bar.k_empty[(n + 1) & 1]);
-                        if (left - j > 1) tc_commit(&bar.v_empty[n & 1]);
+                        if (!C::apart && more) tc_commit(&bar.k_empty[(n + 1) & 1]);
+                        tc_commit(&bar.v_empty[n & 1]);
                     }
                     if (!ok) break;
                     for (int i = 0; i < halves; ++i) ++hs[i];
-                    left -= tiles;
+                    left -= pt.units;
                     if (left > 0) advance(p, at, s);
                 }
+                // nothing of this CTA's may arrive after its end
+                if (n > 0) wait(&bar.v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1);
             }
             __syncwarp();
-        } else if (warp == 13) {
+        } else if (warp == kLoadWarp) {
             // ------------------------------------------------ loader
             // raw tiles in the order K0, then K(j+1), V(j), over the share
-            uint32_t n = 0, r = 0;
+            uint32_t n = 0, st = 0, par = 1;
             auto load = [&](const uint8_t* pool, uint32_t mask, int64_t off) {
-                const uint32_t st = r % kRaw;
                 bool ok = true;
                 if (lane == 0) {
-                    ok = wait(&bar.raw_empty[st], ((r / kRaw) & 1) ^ 1);
+                    ok = wait(&bar.raw_empty[st], par);
                     if (ok) mbar_arrive_expect_tx(&bar.raw_full[st], __popc(mask) * 16 * RB);
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (ok && ((mask >> lane) & 1u)) bulk_g2s(smem + C::kRaw0 + st * C::kRawB + lane * 16 * RB, pool + off, 16 * RB, &bar.raw_full[st]);
-                ++r;
+                if (++st == kRaw) {
+                    st = 0;
+                    par ^= 1;
+                }
             };
             uint32_t vmask = 0;    // of the tile whose values come next
             int64_t voff = 0;
             bool pending = false;
             while (left > 0) {
                 const Span sp = span_of(p, s, at.rt);
-                const int tiles = min(left, sp.n - at.tile);
-                for (int j = 0; j < tiles; ++j, ++n) {
+                const Part pt = part_of(at, sp, left);
+                for (int j = 0; j < pt.n; ++j, ++n) {
                     // lane i < 8: keys 16 i .. of the tile
-                    const int key = (sp.t0 + at.tile + j) * kKeys + 16 * lane;
+                    const int key = (sp.t0 + pt.t0 + j) * kKeys + 16 * lane;
                     int64_t off = 0;
                     bool in = lane < 8 && key < s.len && key + 16 > sp.lo;
                     if (in) {
-                        const int blk = key / p.page;
+                        const int blk = page_of(p, key);
                         const int pg = p.table[static_cast<int64_t>(at.b) * p.max_blocks + blk];
                         if (pg < 0 || pg >= p.n_pages) {
                             in = false;
@@ -454,56 +555,69 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                     voff = off;
                     pending = true;
                 }
-                left -= tiles;
+                left -= pt.units;
                 if (left > 0) advance(p, at, s);
             }
             if (pending) load(p.vp, vmask, voff);
         }
-    } else if (warp >= 8) {
-        regs_dec<88>();
+    } else if (warp >= kSoft) {
+        regs_dec<48>();
         // ---------------------------------------------------- decoders
-        const int row = tid - 256;
-        uint32_t r = 0, n = 0;
+        // thread = key and half of its blocks
+        const int row = tid & 127, side = (warp - kSoft) >> 2;
+        uint32_t st = 0, par = 0, n = 0, seg = 0;
         const uint32_t sw = (row & 7) << 4;
-        // tile number m of `dst`, from raw tile r; the key is there or zero
-        auto decode = [&](uint32_t base, uint64_t* full, uint64_t* empty, uint32_t m, bool there) {
-            const uint32_t st = r % kRaw;
-            bool ok = wait(&bar.raw_full[st], (r / kRaw) & 1);
+        // tile number m into `base`, from the next raw tile; a key that is not
+        // there is zero, and so is a value block whose scale is not finite (its
+        // key is noted for the rows of segment vseg, before the tile is handed over)
+        bool vthere = false;
+        int vkey = 0;
+        uint32_t vseg = 0;
+        auto decode = [&](uint32_t base, uint64_t* full, uint64_t* empty, uint32_t m, bool there, bool value) {
+            bool ok = wait(&bar.raw_full[st], par);
             ok = wait(&empty[m & 1], ((m >> 1) & 1) ^ 1) && ok;
             ok = __all_sync(0xffffffffu, ok);
+            bool bad = false;
             if (ok) {
-                const uint32_t src = sb + C::kRaw0 + st * C::kRawB + row * RB;
-                uint32_t w[9 * NB / 2];
-                if constexpr (NB % 4 == 0) {
+                // NB = 4: a pair of blocks, 9 words; NB = 2: the even block's words
+                // 0..4 or the odd one's 4..8
+                const uint32_t src = sb + C::kRaw0 + st * C::kRawB + row * RB + side * (NB == 4 ? 36 : 16);
+                constexpr int W = NB == 4 ? 9 : 5;
+                uint32_t x[W];
 #pragma unroll
-                    for (int i = 0; i < 9 * NB / 4; ++i) {
-                        const uint2 v = lds64(src + 8 * i);
-                        w[2 * i] = v.x;
-                        w[2 * i + 1] = v.y;
-                    }
-                } else {
+                for (int i = 0; i < W; ++i) x[i] = lds32(src + 4 * i);
+                const uint32_t dst = base + (m & 1) * C::kTileB + row * 128 + (NB == 4 ? side * C::kHalfB : 0);
 #pragma unroll
-                    for (int i = 0; i < 9 * NB / 2; ++i) w[i] = lds32(src + 4 * i);
-                }
-                const uint32_t dst = base + (m & 1) * C::kTileB + row * 128;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const uint32_t* x = w + 9 * (b >> 1);
-                    uint32_t d = (b & 1) ? __byte_perm(x[4], x[4], 0x3232) : __byte_perm(x[0], x[0], 0x1010);
+                for (int b = 0; b < HB; ++b) {
+                    const bool odd = NB == 4 ? (b & 1) : side != 0;
+                    uint32_t d = NB == 4 ? (b ? __byte_perm(x[4], x[4], 0x3232) : __byte_perm(x[0], x[0], 0x1010))
+                                         : __byte_perm(x[0], x[0], odd ? 0x3232 : 0x1010);
                     if (!there) d = 0;
+                    if (value && (d & 0x7c00u) == 0x7c00u) {
+                        bad = true;
+                        d = 0;
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint32_t c = (b & 1) ? x[5 + i] : (i < 3 ? x[1 + i] : __byte_perm(x[0], x[4], 0x5432));
+                        uint32_t c;
+                        if constexpr (NB == 4) {
+                            c = b ? x[(5 + i) % W] : (i < 3 ? x[1 + i] : __byte_perm(x[0], x[4], 0x5432));
+                        } else {
+                            c = i < 3 ? x[1 + i] : (odd ? x[4] : __byte_perm(x[0], x[4], 0x5432));
+                        }
                         const uint32_t e = c >> 8;
                         // 1024 + code - 1032 and (1024 + 16 code) / 16 - 72: code - 8, exact
                         const uint32_t v0 = hsub2_u32(and_or(c, 0x000f000fu, 0x64006400u), 0x64086408u);
                         const uint32_t v1 = hfma2_u32(and_or(c, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
                         const uint32_t v2 = hsub2_u32(and_or(e, 0x000f000fu, 0x64006400u), 0x64086408u);
                         const uint32_t v3 = hfma2_u32(and_or(e, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
-                        const int ch = 4 * b + i;
-                        sts128(dst + (ch >> 3) * C::kHalfB + (((ch & 7) << 4) ^ sw), hmul2_u32(v0, d), hmul2_u32(v1, d),
-                               hmul2_u32(v2, d), hmul2_u32(v3, d));
+                        const uint32_t ch = NB == 4 ? 4 * b + i : 4 * side + i;
+                        sts128(dst + ((ch << 4) ^ sw), hmul2_u32(v0, d), hmul2_u32(v1, d), hmul2_u32(v2, d), hmul2_u32(v3, d));
                     }
+                }
+                if (bad) {
+                    atomicMin(&bad_lo[vseg & 7], vkey);
+                    atomicMax(&bad_hi[vseg & 7], vkey);
                 }
                 fence_proxy_async();
             }
@@ -512,201 +626,269 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                 mbar_arrive(&bar.raw_empty[st]);
                 mbar_arrive(&full[m & 1]);
             }
-            ++r;
+            if (++st == kRaw) {
+                st = 0;
+                par ^= 1;
+            }
         };
-        bool pending = false, vthere = false;
+        bool pending = false;
+        auto values = [&]() { decode(sb + C::kV, bar.v_full, bar.v_empty, n - 1, vthere, true); };
         while (left > 0) {
             const Span sp = span_of(p, s, at.rt);
-            const int tiles = min(left, sp.n - at.tile);
-            for (int j = 0; j < tiles; ++j, ++n) {
-                const int key = (sp.t0 + at.tile + j) * kKeys + row;
-                // the loader's mask is read after its raw tile is full
-                const uint32_t st = r % kRaw;
-                wait(&bar.raw_full[st], (r / kRaw) & 1);
-                const bool there = key < s.len && ((reinterpret_cast<volatile uint32_t*>(tmask)[n & 15] >> (row >> 4)) & 1u);
-                decode(sb + C::kK, bar.k_full, bar.k_empty, n, there);
-                if (pending) decode(sb + C::kV, bar.v_full, bar.v_empty, n - 1, vthere);
+            const Part pt = part_of(at, sp, left);
+            for (int j = 0; j < pt.n; ++j, ++n) {
+                const int key = (sp.t0 + pt.t0 + j) * kKeys + row;
+                wait(&bar.raw_full[st], par);   // the loader's mask is there with the raw tile
+                const bool there = key < s.len && key >= sp.lo && ((tmask[n & 15] >> (row >> 4)) & 1u);
+                decode(sb + C::kK, bar.k_full, bar.k_empty, n, there, false);
+                if (pending) values();
                 vthere = there;
+                vkey = key;
+                vseg = seg;
                 pending = true;
             }
-            left -= tiles;
+            seg += pt.n > 0;
+            left -= pt.units;
             if (left > 0) advance(p, at, s);
         }
-        if (pending) decode(sb + C::kV, bar.v_full, bar.v_empty, n - 1, vthere);
+        if (pending) values();
     } else {
-        regs_inc<184>();
+        regs_inc<88>();
         // ------------------------------------------------------ softmax
-        const int half = warp >> 2, row = tid & 127;
+        // Two threads a row: keys 0..63 and 64..127 of every tile (`side`), the
+        // first and second half of q's and the output's values.
+        const int half = warp >> 3, side = (warp >> 2) & 1, row = 32 * (warp & 3) + lane, pr = 128 * half + row;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // this warp's 32 lanes of tensor memory
-        const uint32_t ts = tmem + half * 128 + lanes, to = tmem + 256 + half * D + lanes;
+        const uint32_t ts = tmem + half * 128 + 64 * side + lanes;
+        const uint32_t tp = tmem + C::kP + half * C::kPHalf + 32 * side + lanes;
+        const uint32_t to = tmem + C::kO + half * D + D / 2 * side + lanes;
+        // exchange with the row's other thread: double-buffered, so that one
+        // barrier of the two warps is enough
+        float* ex = reinterpret_cast<float*>(smem + C::kEx) + pr;
+        uint32_t flip = 0;
+        const int pair = 1 + 4 * half + (warp & 3);
+        auto other = [&](float v) {
+            ex[(flip + side) * kRows] = v;
+            asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+            const float o = ex[(flip + (side ^ 1)) * kRows];
+            flip ^= 2;
+            return o;
+        };
         uint32_t n = 0;                // tiles so far
-        uint32_t hn = 0, hs = 0;       // tiles and segments of this half
+        uint32_t hn = 0, seg = 0;      // tiles of this half, segments
         int slot = 0;
-        while (left > 0) {
+        for (; left > 0;) {
             const Span sp = span_of(p, s, at.rt);
-            const int tiles = min(left, sp.n - at.tile);
-            const bool whole = tiles == sp.n;
-            const bool used = half == 0 || s.rows - at.rt * kRows > 128;
-            const int rr = at.rt * kRows + half * 128 + row;
-            const bool there = rr < s.rows;
-            const int ti = there ? rr / p.group : 0;
-            const int64_t qhead = static_cast<int64_t>(at.h) * p.group + (there ? rr - ti * p.group : 0);
-            const int pos = s.len - s.qlen + ti;
-            int hi = p.causal ? min(pos, s.len - 1) : s.len - 1;
-            int lo = p.window > 0 ? pos - p.window + 1 : 0;
-            if (!there) {
-                hi = 0x7fffffff;
-                lo = 0;
-            }
-            // ---- q: scaled by a power of two, in the blocks' order
-            float c = 1.f;       // of S, to base-2 scores
+            const Part pt = part_of(at, sp, left);
+            const int tiles = pt.n;
+            const bool used = tiles > 0 && (half == 0 || s.rows - at.rt * kRows > 128);
             if (used) {
-                const uint16_t* src = p.q + (s.tok0 + ti) * p.q_stride + qhead * D;
-                uint32_t w[D / 2];
-                uint32_t mx = 0;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 v = there ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
-                    w[4 * i] = v.x;
-                    w[4 * i + 1] = v.y;
-                    w[4 * i + 2] = v.z;
-                    w[4 * i + 3] = v.w;
-                    mx = absmax8_bf16(mx, v);
+                const bool whole = tiles == sp.n;
+                const int rr = at.rt * kRows + pr;
+                const bool there = rr < s.rows;
+                const int ti = there ? group_of(p, rr) : 0;
+                const int64_t qhead = static_cast<int64_t>(at.h) * p.group + (there ? rr - ti * p.group : 0);
+                const int pos = s.len - s.qlen + ti;
+                int hi = p.causal ? min(pos, s.len - 1) : s.len - 1;
+                int lo = p.window > 0 ? pos - p.window + 1 : 0;
+                if (!there) {
+                    hi = 0x7fffffff;
+                    lo = 0;
                 }
-                mx = max(mx & 0xffffu, mx >> 16);
-                if (mx >= 0x7f80u && p.err) atomicOr(p.err, KQ_DEV_X_RANGE);
-                const int e = xscale_exp(mx, 13);
-                // the scale's sign goes into q, so that c > 0; scale 0: q = 0
-                const float up = p.scale == 0.f ? 0.f : copysignf(exp2_int(e), p.scale);
-                c = p.scale == 0.f ? 1.f : fmaxf(fabsf(p.scale) * exp2_int(-e), 1.17549435e-38f);
-                const uint32_t dst = sb + C::kQ + half * C::kTileB + row * 128;
+                // keys that every row of this warp sees
+                const int all_hi = __reduce_min_sync(0xffffffffu, hi), all_lo = __reduce_max_sync(0xffffffffu, lo);
+                // ---- q: scaled by a power of two, in the blocks' order
+                float c = 1.f;       // of S, to base-2 scores
+                {
+                    const uint16_t* src = p.q + (s.tok0 + ti) * p.q_stride + qhead * D + D / 2 * side;
+                    uint32_t w[D / 4];
+                    uint32_t mx = 0;
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint4 v = there ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+                        w[4 * i] = v.x;
+                        w[4 * i + 1] = v.y;
+                        w[4 * i + 2] = v.z;
+                        w[4 * i + 3] = v.w;
+                        mx = absmax8_bf16(mx, v);
+                    }
+                    mx = max(mx & 0xffffu, mx >> 16);
+                    if (mx >= 0x7f80u && p.err) atomicOr(p.err, KQ_DEV_X_RANGE);
+                    mx = max(mx, __float_as_uint(other(__uint_as_float(mx))));
+                    const int e = xscale_exp(mx, 13);
+                    // the scale's sign goes into q, so that c > 0; scale 0: q = 0
+                    const float up = p.scale == 0.f ? 0.f : copysignf(exp2_int(e), p.scale);
+                    c = p.scale == 0.f ? 1.f : fmaxf(fabsf(p.scale) * exp2_int(-e), 1.17549435e-38f);
+                    const uint32_t dst = sb + C::kQ + half * C::kTileB + row * 128 + (NB == 4 ? side * C::kHalfB : 0);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t o[4];
+                    for (int b = 0; b < HB; ++b)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            float f[2];
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t o[4];
 #pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                const int v = 32 * b + value_of(b, i, 2 * k + z);
-                                f[z] = ((v & 1) ? bf16hi_to_f32(w[v >> 1]) : bf16lo_to_f32(w[v >> 1])) * up;
+                            for (int k = 0; k < 4; ++k) {
+                                float f[2];
+#pragma unroll
+                                for (int z = 0; z < 2; ++z) {
+                                    // (NB = 2: the side is the block's parity)
+                                    const int v0 = 32 * b + value_of(NB == 4 ? b : 0, i, 2 * k + z);
+                                    const int v1 = 32 * b + value_of(NB == 4 ? b : 1, i, 2 * k + z);
+                                    const float a0 = (v0 & 1) ? bf16hi_to_f32(w[v0 >> 1]) : bf16lo_to_f32(w[v0 >> 1]);
+                                    const float a1 = (v1 & 1) ? bf16hi_to_f32(w[v1 >> 1]) : bf16lo_to_f32(w[v1 >> 1]);
+                                    f[z] = (NB == 2 && side ? a1 : a0) * up;
+                                }
+                                o[k] = pack_f16x2(f[0], f[1]);
                             }
-                            o[k] = pack_f16x2(f[0], f[1]);
+                            const uint32_t ch = NB == 4 ? 4 * b + i : 4 * side + i;
+                            sts128(dst + ((ch << 4) ^ ((row & 7) << 4)), o[0], o[1], o[2], o[3]);
                         }
-                        const int ch = 4 * b + i;
-                        sts128(dst + (ch >> 3) * C::kHalfB + (((ch & 7) << 4) ^ ((row & 7) << 4)), o[0], o[1], o[2], o[3]);
-                    }
-                fence_proxy_async();
-                tc_fence_before();
-                mbar_arrive(&bar.q_full[half]);
-            }
-            float m = -INFINITY;     // reference of the exponents, times c
-            float2 l2 = make_float2(0.f, 0.f);
-            for (int j = 0; used && j < tiles; ++j) {
-                if (!__all_sync(0xffffffffu, wait(&bar.s_full[half], (hn + j) & 1))) break;
-                tc_fence_after();
-                uint32_t x[128];
-                tmem_ld64(ts, x);
-                tmem_ld64(ts + 64, x + 64);
-                const int key0 = (sp.t0 + at.tile + j) * kKeys;
-                const uint32_t mask = reinterpret_cast<volatile uint32_t*>(tmask)[(n + j) & 15];
-                if (__any_sync(0xffffffffu, key0 + kKeys - 1 > hi || key0 < lo || mask != 0xffu)) {
-                    const int h0 = hi - key0, l0 = lo - key0;
-#pragma unroll
-                    for (int k = 0; k < 128; ++k)
-                        if (k > h0 || k < l0 || !((mask >> (k >> 4)) & 1u)) x[k] = 0xff800000u;
+                    fence_proxy_async();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.q_full[half]);
                 }
-                float mt = __uint_as_float(x[0]);
+                float m = -INFINITY;     // reference of the exponents, times c
+                float2 l2 = make_float2(0.f, 0.f);
+                for (int j = 0; j < tiles; ++j) {
+                    // (where a wait has run out the CTA goes through its barriers all
+                    // the same, on whatever is there)
+                    wait(&bar.s_full[half], (hn + j) & 1);
+                    __syncwarp();
+                    tc_fence_after();
+                    uint32_t x[64];
+                    tmem_ld32(ts, x);
+                    tmem_ld32(ts + 32, x + 32);
+                    if (C::apart && j + 1 < tiles) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.s_free[half]);
+                    }
+                    const int key0 = (sp.t0 + pt.t0 + j) * kKeys + 64 * side;
+                    const uint32_t mask = (tmask[(n + j) & 15] >> (4 * side)) & 15u;
+                    if (key0 + 63 > all_hi || key0 < all_lo || mask != 15u) {
 #pragma unroll
-                for (int k = 1; k < 128; ++k) mt = fmaxf(mt, __uint_as_float(x[k]));
-                mt *= c;
-                if (__any_sync(0xffffffffu, mt > m + kLazy)) {
-                    const float nm = fmaxf(m, mt);
-                    const float f = m == nm ? 1.f : ex2(m - nm);
-                    m = nm;
-                    l2.x *= f;
-                    l2.y *= f;
-                    if (j > 0) {
+                        for (int w = 0; w < 2; ++w) {
+                            // bits of the keys that this row sees
+                            const int h0 = hi - key0 - 32 * w, l0 = lo - key0 - 32 * w;
+                            uint32_t bits = h0 < 0 ? 0u : (h0 >= 31 ? ~0u : (2u << h0) - 1u);
+                            bits &= l0 <= 0 ? ~0u : (l0 > 31 ? 0u : ~0u << l0);
+                            bits &= ((mask >> (2 * w)) & 1u ? 0xffffu : 0u) | ((mask >> (2 * w)) & 2u ? 0xffff0000u : 0u);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!((bits >> k) & 1u)) x[32 * w + k] = 0xff800000u;
+                        }
+                    }
+                    float mx[4];     // (one chain would wait for each step)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 4]));
+#pragma unroll
+                    for (int k = 8; k < 64; k += 8)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            mx[z] = fmaxf(mx[z], fmaxf(__uint_as_float(x[k + z]), __uint_as_float(x[k + z + 4])));
+                    float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                    // (the barrier also shows that both sides have read S, over
+                    // which P goes)
+                    mt = fmaxf(mt, other(mt));
+                    // P V of the tile before is done with P and O
+                    if (j > 0) wait(&bar.o_full[half], (hn + j - 1) & 1);
+                    __syncwarp();
+                    tc_fence_after();
+                    if (__any_sync(0xffffffffu, mt > m + kLazy)) {
+                        const float nm = fmaxf(m, mt);
+                        const float f = m == nm ? 1.f : ex2(m - nm);
+                        m = nm;
+                        l2.x *= f;
+                        l2.y *= f;
+                        if (j > 0) {
 #pragma unroll 1
-                        for (int k = 0; k < D / 32; ++k) {
-                            uint32_t o[32];
-                            tmem_ld32(to + 32 * k, o);
+                            for (int k = 0; k < D / 32; ++k) {
+                                uint32_t o[16];
+                                tmem_ld16(to + 16 * k, o);
 #pragma unroll
-                            for (int z = 0; z < 32; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
-                            tmem_st32(to + 32 * k, o);
+                                for (int z = 0; z < 16; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
+                                tmem_st16(to + 16 * k, o);
+                            }
                         }
                     }
-                }
-                const float bias = m == -INFINITY ? 0.f : kPBias - m;
-                const float2 c2 = make_float2(c, c), b2 = make_float2(bias, bias);
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    uint32_t pk[32];
+                    const float bias = m == -INFINITY ? 0.f : kPBias - m;
+                    const float2 cc = make_float2(c, c), bb = make_float2(bias, bias);
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
-                        float2 y = make_float2(__uint_as_float(x[64 * z + 2 * k]), __uint_as_float(x[64 * z + 2 * k + 1]));
-                        y = fma2(y, c2, b2);
+                        float2 y = make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+                        y = fma2(y, cc, bb);
                         y.x = ex2(y.x);
                         y.y = ex2(y.y);
                         l2 = add2(l2, y);
-                        pk[k] = pack_f16x2(y.x, y.y);
+                        x[k] = pack_f16x2(y.x, y.y);
                     }
-                    tmem_st32(ts + 32 * z, pk);
+                    tmem_st32(tp, x);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.p_full[2 * half + side]);
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(&bar.p_full[half]);
-            }
-            // ---- output
-            const float l = l2.x + l2.y;
-            if (used && __all_sync(0xffffffffu, wait(&bar.o_full[half], hs & 1))) {
-                tc_fence_after();
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                float* part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * C::kSlot;
-                const int pr = half * 128 + row;
-                uint16_t* out = p.out + (static_cast<int64_t>(s.tok0 + ti) * p.n_heads + qhead) * D;
+                // ---- output
+                float l = l2.x + l2.y;
+                l += other(l);
+                if (__all_sync(0xffffffffu, wait(&bar.o_full[half], (hn + tiles - 1) & 1))) {
+                    tc_fence_after();
+                    // a row that sees a key whose value scale is not finite
+                    if (bad_hi[seg & 7] >= lo && bad_lo[seg & 7] <= hi && there) l = __int_as_float(0x7fc00000);
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    float* part = parts_of(p) + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * C::kSlot;
+                    uint16_t* out = p.out + (static_cast<int64_t>(s.tok0 + ti) * p.n_heads + qhead) * D + D / 2 * side;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    uint32_t o[32];
-                    float v[32];
-                    tmem_ld32(to + 32 * b, o);
+                    for (int b = 0; b < HB; ++b) {
+                        uint32_t o[32];
+                        tmem_ld32(to + 32 * b, o);
+                        auto at_value = [&](int v) {   // value v of the block, from its place in the codes' order
+                            float r = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[value_of(b, i, e)] = __uint_as_float(o[8 * i + e]);
-                    if (whole) {
-                        if (there) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t h[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const __nv_bfloat162 t2 = __floats2bfloat162_rn(v[8 * i + 2 * k] * inv, v[8 * i + 2 * k + 1] * inv);
-                                    h[k] = l == 0.f ? 0u : *reinterpret_cast<const uint32_t*>(&t2);
+                                for (int e = 0; e < 8; ++e) {
+                                    if (NB == 4 && value_of(b, i, e) == v) r = __uint_as_float(o[8 * i + e]);
+                                    if (NB == 2 && value_of(0, i, e) == v && side == 0) r = __uint_as_float(o[8 * i + e]);
+                                    if (NB == 2 && value_of(1, i, e) == v && side == 1) r = __uint_as_float(o[8 * i + e]);
                                 }
-                                *reinterpret_cast<uint4*>(out + 32 * b + 8 * i) = make_uint4(h[0], h[1], h[2], h[3]);
-                            }
-                        }
-                    } else {
+                            return r;
+                        };
+                        if (whole) {
+                            if (there) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<float4*>(part + pr * D + 32 * b + 4 * i) =
-                                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                                for (int i = 0; i < 4; ++i) {
+                                    uint32_t h[4];
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        const __nv_bfloat162 t2 = __floats2bfloat162_rn(at_value(8 * i + 2 * k) * inv, at_value(8 * i + 2 * k + 1) * inv);
+                                        h[k] = l == 0.f ? 0u : *reinterpret_cast<const uint32_t*>(&t2);
+                                    }
+                                    *reinterpret_cast<uint4*>(out + 32 * b + 8 * i) = make_uint4(h[0], h[1], h[2], h[3]);
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<float4*>(part + pr * D + D / 2 * side + 32 * b + 4 * i) =
+                                    make_float4(at_value(4 * i), at_value(4 * i + 1), at_value(4 * i + 2), at_value(4 * i + 3));
+                        }
+                    }
+                    if (!whole && side == 0) {
+                        part[kRows * D + pr] = m;
+                        part[kRows * D + kRows + pr] = l;
                     }
                 }
-                if (!whole) {
-                    part[kRows * D + pr] = m;
-                    part[kRows * D + kRows + pr] = l;
-                }
-            }
-            n += tiles;
-            if (used) {
                 hn += tiles;
-                ++hs;
             }
-            left -= tiles;
+            // the slot of the segment four on is long read, and not yet written
+            if (tiles > 0 && tid == 0) {
+                bad_lo[(seg + 4) & 7] = 0x7fffffff;
+                bad_hi[(seg + 4) & 7] = -1;
+            }
+            seg += tiles > 0;
+            n += tiles;
+            left -= pt.units;
             slot = 1;
             if (left > 0) advance(p, at, s);
         }
@@ -718,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 // Joins the partial results of a segment that spans CTAs, in list order: the
@@ -727,24 +909,16 @@ template <int NB>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const AttnParams p) {
     using C = Shape<NB>;
     constexpr int D = C::D, per = D / 4;
-    __shared__ unsigned long long sum;
-    __shared__ Place place;
     pdl_wait();
-    const int64_t total = list_total(p, &sum);
-    const int64_t share = share_of(total, p.n_ctas);
-    const int64_t u = share * (static_cast<int64_t>(blockIdx.x) + 1);
-    if (u >= total) return;
-    if (threadIdx.x < 32) {
-        const Place at = list_find(p, u);
-        if (threadIdx.x == 0) place = at;
-    }
-    __syncthreads();
-    const Place at = place;
+    const Plan* plan = plan_of(p);
+    const int64_t share = plan->share, u = share * (static_cast<int64_t>(blockIdx.x) + 1);
+    if (u >= plan->total) return;
+    const Place at = plan->at[blockIdx.x + 1];
     const Seq s = seq_of(p, at.b);
-    const int64_t a = at.start, e = a + span_of(p, s, at.rt).n;
-    if (a == u || u - share > a) return;   // not cut here, or cut before
-    const int c0 = static_cast<int>(a / share), c1 = static_cast<int>((e - 1) / share);
-    auto slot = [&](int c) { return p.part + (static_cast<int64_t>(c) * 2 + (c > c0 || a == c * share ? 0 : 1)) * C::kSlot; };
+    const int64_t a = at.start, t = a + kSegCost, e = t + span_of(p, s, at.rt).n;   // units: the segment, its tiles
+    if (t >= u || u - share > t) return;   // its tiles are not cut here, or cut before
+    const int c0 = static_cast<int>(t / share), c1 = static_cast<int>((e - 1) / share);
+    auto slot = [&](int64_t c) { return parts_of(p) + (c * 2 + (c * share >= a ? 0 : 1)) * C::kSlot; };   // (0: the share's first segment)
     for (int i = threadIdx.x; i < 8 * per; i += 256) {
         const int r = blockIdx.y * 8 + i / per, c4 = (i % per) * 4, rr = at.rt * kRows + r;
         if (rr >= s.rows) continue;
@@ -766,17 +940,19 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const AttnParams p) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const __nv_bfloat162 x = __floats2bfloat162_rn(v.x * inv, v.y * inv);
         const __nv_bfloat162 z = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-        const int ti = rr / p.group;
+        const int ti = group_of(p, rr);
         const int64_t row = static_cast<int64_t>(s.tok0 + ti) * p.n_heads + at.h * p.group + (rr - ti * p.group);
         *reinterpret_cast<uint2*>(p.out + row * D + c4) = l == 0.f ? make_uint2(0, 0) :
             make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&z));
     }
 }
 
+int prompt_ctas() { return device_sm_count() < kMostCtas ? device_sm_count() : kMostCtas; }
+
 template <int NB>
 int launch_of(AttnParams p, cudaStream_t s) {
     using C = Shape<NB>;
-    p.n_ctas = device_sm_count();
+    p.n_ctas = prompt_ctas();
     static bool ready[64] = {};   // the attribute is set once a device
     int dev = 0;
     int rc = record_cuda(cudaGetDevice(&dev));
@@ -786,6 +962,8 @@ int launch_of(AttnParams p, cudaStream_t s) {
         if (rc) return rc;
         if (dev < 64) ready[dev] = true;
     }
+    rc = launch_pdl(prompt_plan_kernel, dim3(1), 256, 0, s, p);
+    if (rc) return rc;
     rc = launch_pdl(prompt_kernel<NB>, dim3(static_cast<unsigned>(p.n_ctas)), kThreads, C::kSmem, s, p);
     if (rc || p.n_ctas == 1) return rc;
     return launch_pdl(prompt_join_kernel<NB>, dim3(static_cast<unsigned>(p.n_ctas - 1), kRows / 8), 256, 0, s, p);
@@ -796,7 +974,7 @@ int launch_of(AttnParams p, cudaStream_t s) {
 bool kv_prompt_covers(int head_dim) { return head_dim == 64 || head_dim == 128; }
 
 int64_t kv_prompt_workspace(int head_dim) {
-    return static_cast<int64_t>(device_sm_count()) * 2 * (kRows * head_dim + 2 * kRows) * 4;
+    return kPlanBytes + static_cast<int64_t>(prompt_ctas()) * 2 * (kRows * head_dim + 2 * kRows) * 4;
 }
 
 int launch_kv_prompt(AttnParams p, int head_dim, cudaStream_t s) {
