@@ -15,6 +15,7 @@ activations ``bfloat16 [M, K]``, outputs ``float32``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -92,7 +93,13 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle without a Stream object around it (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     s = torch.cuda.current_stream() if stream is None else stream
     return s.cuda_stream
 
@@ -100,10 +107,12 @@ def _stream(stream=None) -> int:
 def _need_cuda(*ts):
     # contiguity first: a strided view (say, some rows of every expert of a
     # bank) would otherwise be walked with the packed stride
-    if any(t is not None and not t.is_contiguous() for t in ts):
-        raise ValueError("all tensors must be contiguous")
-    if any(t is not None and not t.is_cuda for t in ts):
-        raise ValueError("all tensors must be CUDA tensors")
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("all tensors must be contiguous")
+    for t in ts:
+        if t is not None and not t.is_cuda:
+            raise ValueError("all tensors must be CUDA tensors")
 
 
 def _need(t, what: str, size: int, count: int | None = None, exact: bool = False) -> None:
@@ -355,30 +364,59 @@ def moe_glu_gather(x: torch.Tensor, gate_bank: torch.Tensor, up_bank: torch.Tens
 # one for keys and one for values; a slot is page * page_size + offset.
 
 
-def _same_device(*ts) -> torch.device:
-    dev = {t.device for t in ts if t is not None}
-    if len(dev) != 1:
-        raise ValueError(f"all tensors must be on one device, got {sorted(map(str, dev))}")
-    return dev.pop()
+def _place(*ts) -> int:
+    """Index of the CUDA device that holds all of the tensors (None: absent),
+    which are contiguous."""
+    dev = None
+    for t in ts:
+        if t is not None:
+            if not t.is_contiguous():
+                raise ValueError("all tensors must be contiguous")
+            d = t.get_device()
+            if dev is None:
+                dev = d
+            elif d != dev:
+                raise ValueError("all tensors must be on one device")
+    if dev < 0:
+        raise ValueError("all tensors must be CUDA tensors")
+    return dev
 
 
-def _call(dev: torch.device, stream, what: str, *args) -> None:
-    """The library call ``what`` on ``dev`` and that device's current stream (or ``stream``)."""
+def _call(dev: int, stream, what: str, *args) -> None:
+    """The library call ``what`` on device ``dev`` and its current stream (or ``stream``)."""
     f = getattr(lib(), what)
-    if dev.index == torch.cuda.current_device():
-        _check(f(*args, _stream(stream)), what)
+    if dev == torch.cuda.current_device():
+        rc = f(*args, _stream(stream))
     else:
         with torch.cuda.device(dev):
-            _check(f(*args, _stream(stream)), what)
+            rc = f(*args, _stream(stream))
+    if rc:
+        raise KQError(rc, what)
 
 
-def _scratch(dev: torch.device, stream, *shape, dtype=torch.int32) -> torch.Tensor:
-    """Memory of the stream that the call runs on (the caching allocator gives
-    freed memory to later work of the stream it was allocated on only)."""
+def _scratch(like: torch.Tensor, stream, size, dtype=torch.int32) -> torch.Tensor:
+    """Memory on the device of ``like``, of the stream that the call runs on (the
+    caching allocator gives freed memory to later work of the stream it was
+    allocated on only)."""
     if stream is None:
-        return torch.empty(*shape, dtype=dtype, device=dev)
+        return torch.empty(size, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(*shape, dtype=dtype, device=dev)
+        return torch.empty(size, dtype=dtype, device=like.device)
+
+
+def _need_pools(k_pool: torch.Tensor, v_pool: torch.Tensor, qtype: int, heads: int | None, dim: int) -> torch.Size:
+    """Shape of the two pools (heads None: whatever the pools have)."""
+    shape = k_pool.shape
+    if (qtype == Q4_0 and len(shape) == 4 and shape[3] * 16 == dim * 9 and (heads is None or shape[1] == heads)
+            and v_pool.shape == shape and k_pool.dtype is torch.uint8 and v_pool.dtype is torch.uint8):
+        return shape
+    if heads is None:
+        heads = shape[1] if len(shape) == 4 else 0
+    _need_pool(k_pool, "k_pool", qtype, heads, dim)
+    _need_pool(v_pool, "v_pool", qtype, heads, dim)
+    if v_pool.shape != shape:
+        raise ValueError(f"v_pool: shape {tuple(shape)} expected, got {tuple(v_pool.shape)}")
+    return shape
 
 
 def _need_pool(pool: torch.Tensor, what: str, qtype: int, heads: int, dim: int) -> None:
@@ -395,9 +433,10 @@ def _token_rows(x: torch.Tensor, what: str) -> int:
     if x.dim() != 3:
         raise ValueError(f"{what}: [tokens, heads, head_dim] expected, got {tuple(x.shape)}")
     t, h, d = x.shape
-    if (d > 1 and x.stride(2) != 1) or (h > 1 and x.stride(1) != d):
+    st, sh, sd = x.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
         raise ValueError(f"{what}: heads and values of a token must be contiguous")
-    return x.stride(0) if t > 1 else h * d
+    return st if t > 1 else h * d
 
 
 def kv_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -410,26 +449,32 @@ def kv_plan(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torc
     (default: taken itself).  Slots and positions behind the last token are -1.
     What does not fit gets slot -1 and sets DEV_TOO_MANY in err."""
     n = cached_lens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != n:
-        raise ValueError(f"block_table: [{n}, max_blocks] expected, got {tuple(block_table.shape)}")
+    table = block_table.shape
+    if len(table) != 2 or table[0] != n:
+        raise ValueError(f"block_table: [{n}, max_blocks] expected, got {tuple(table)}")
     if taken_out is None:
         taken_out = taken
-    for t, what, count in ((cached_lens, "cached_lens", n), (new_lens, "new_lens", n), (block_table, "block_table", None),
-                           (free_pages, "free_pages", None), (taken, "taken", 1), (taken_out, "taken_out", 1), (err, "err", 1)):
-        _need(t, what, 4, count)
-    _need_cuda(cached_lens, new_lens, block_table, free_pages, taken, taken_out, err)
-    dev = _same_device(cached_lens, new_lens, block_table, free_pages, taken, taken_out, err)
+    i32 = torch.int32
+    if not (cached_lens.dtype is i32 and new_lens.dtype is i32 and block_table.dtype is i32 and free_pages.dtype is i32
+            and taken.dtype is i32 and taken_out.dtype is i32 and new_lens.numel() >= n and taken.numel() and taken_out.numel()
+            and err is None):
+        for t, what, count in ((cached_lens, "cached_lens", n), (new_lens, "new_lens", n), (block_table, "block_table", None),
+                               (free_pages, "free_pages", None), (taken, "taken", 1), (taken_out, "taken_out", 1), (err, "err", 1)):
+            _need(t, what, 4, count)
+    dev = _place(cached_lens, new_lens, block_table, free_pages, taken, taken_out, err)
     cap = int(cap)
     if cap < 0:
         raise ValueError(f"cap must not be negative, got {cap}")
-    seq, cu, first, slots, pos = _scratch(dev, stream, 3 * n + 1 + 2 * cap).split([n, n + 1, n, cap, cap])
-    _call(dev, stream, "kq_kv_plan", _ptr(cached_lens), _ptr(new_lens), n, page_size, _ptr(block_table),
-          block_table.shape[1], _ptr(free_pages), free_pages.numel(), _ptr(taken), _ptr(taken_out), _ptr(seq), _ptr(cu),
-          _ptr(first), _ptr(slots), _ptr(pos), cap, _ptr(err))
+    buf = _scratch(cached_lens, stream, 3 * n + 1 + 2 * cap)
+    seq, cu, slots, pos, _ = buf.split([n, n + 1, cap, cap, n])
+    at = buf.data_ptr()
+    _call(dev, stream, "kq_kv_plan", cached_lens.data_ptr(), new_lens.data_ptr(), n, page_size, block_table.data_ptr(),
+          table[1], free_pages.data_ptr(), free_pages.numel(), taken.data_ptr(), taken_out.data_ptr(),
+          at, at + 4 * n, at + 4 * (2 * n + 1 + 2 * cap), at + 4 * (2 * n + 1), at + 4 * (2 * n + 1 + cap), cap, _ptr(err))
     return seq, cu, slots, pos
 
 
-_F32, _BF16 = 0, 30  # ggml type ids of plain values
+_PLAIN = {torch.float32: 0, torch.bfloat16: 30}  # ggml type ids of plain values
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, qtype: int,
@@ -438,22 +483,19 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_pool: torch.Tensor, v_pool: to
     fused product's columns are fine) into the pools' slots; slot -1: left out."""
     if k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError(f"k and v must have one shape and type, got {tuple(k.shape)} {k.dtype}, {tuple(v.shape)} {v.dtype}")
-    if k.dtype not in (torch.float32, torch.bfloat16):
+    kind = _PLAIN.get(k.dtype)
+    if kind is None:
         raise TypeError("keys and values must be float32 or bfloat16")
     ks, vs = _token_rows(k, "k"), _token_rows(v, "v")
     t, h, d = k.shape
-    _need_pool(k_pool, "k_pool", qtype, h, d)
-    _need_pool(v_pool, "v_pool", qtype, h, d)
-    if k_pool.shape != v_pool.shape:
-        raise ValueError(f"v_pool: shape {tuple(k_pool.shape)} expected, got {tuple(v_pool.shape)}")
+    pool = _need_pools(k_pool, v_pool, qtype, h, d)
     _need(slot_map, "slot_map", 4, t)
     _need(err, "err", 4, 1)
-    _need_cuda(k_pool, v_pool, slot_map, err)
-    if not (k.is_cuda and v.is_cuda):
-        raise ValueError("all tensors must be CUDA tensors")
-    dev = _same_device(k, v, k_pool, v_pool, slot_map, err)
-    _call(dev, stream, "kq_kv_append", qtype, _ptr(k), _ptr(v), _F32 if k.dtype == torch.float32 else _BF16, t, ks, vs, h, d,
-          _ptr(slot_map), _ptr(k_pool), _ptr(v_pool), k_pool.shape[0], k_pool.shape[2], _ptr(err))
+    dev = _place(k_pool, v_pool, slot_map, err)
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("all tensors must be on one device")
+    _call(dev, stream, "kq_kv_append", qtype, k.data_ptr(), v.data_ptr(), kind, t, ks, vs, h, d, slot_map.data_ptr(),
+          k_pool.data_ptr(), v_pool.data_ptr(), pool[0], pool[2], _ptr(err))
 
 
 def kv_attention_workspace(n_heads: int, n_kv_heads: int, head_dim: int, max_new: int) -> int:
@@ -462,6 +504,12 @@ def kv_attention_workspace(n_heads: int, n_kv_heads: int, head_dim: int, max_new
     _check(lib().kq_kv_attention_workspace(n_heads, n_kv_heads, head_dim, max_new, ctypes.byref(b)),
            "kq_kv_attention_workspace")
     return b.value
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(dev: int, n_heads: int, n_kv_heads: int, head_dim: int, max_new: int) -> int:
+    with torch.cuda.device(dev):
+        return kv_attention_workspace(n_heads, n_kv_heads, head_dim, max_new)
 
 
 def kv_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, qtype: int, block_table: torch.Tensor,
@@ -476,35 +524,28 @@ def kv_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, qt
     q = _bf16_bits(q)
     qs = _token_rows(q, "q")
     t, hq, d = q.shape
-    h = k_pool.shape[1] if k_pool.dim() == 4 else 0
-    _need_pool(k_pool, "k_pool", qtype, h, d)
-    _need_pool(v_pool, "v_pool", qtype, h, d)
-    if k_pool.shape != v_pool.shape:
-        raise ValueError(f"v_pool: shape {tuple(k_pool.shape)} expected, got {tuple(v_pool.shape)}")
+    pages, h, page_size, _ = _need_pools(k_pool, v_pool, qtype, None, d)
     n = seq_lens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != n:
-        raise ValueError(f"block_table: [{n}, max_blocks] expected, got {tuple(block_table.shape)}")
-    _need(block_table, "block_table", 4)
-    _need(seq_lens, "seq_lens", 4)
-    _need(cu_new, "cu_new", 4, n + 1)
-    _need(err, "err", 4, 1)
+    table = block_table.shape
+    if len(table) != 2 or table[0] != n:
+        raise ValueError(f"block_table: [{n}, max_blocks] expected, got {tuple(table)}")
+    i32 = torch.int32
+    if not (block_table.dtype is i32 and seq_lens.dtype is i32 and cu_new.dtype is i32 and cu_new.numel() > n and err is None):
+        _need(block_table, "block_table", 4)
+        _need(seq_lens, "seq_lens", 4)
+        _need(cu_new, "cu_new", 4, n + 1)
+        _need(err, "err", 4, 1)
     if out is not None:
         _need(out, "out", 2, t * hq * d)
-    if not q.is_cuda:
-        raise ValueError("all tensors must be CUDA tensors")
-    _need_cuda(k_pool, v_pool, block_table, seq_lens, cu_new, out, workspace, err)
-    dev = _same_device(q, k_pool, v_pool, block_table, seq_lens, cu_new, out, workspace, err)
+    dev = _place(k_pool, v_pool, block_table, seq_lens, cu_new, out, workspace, err)
+    if q.get_device() != dev:
+        raise ValueError("all tensors must be on one device")
     if out is None:
-        out = torch.empty(t, hq, d, dtype=q.dtype, device=dev)
+        out = _scratch(q, stream, (t, hq, d), q.dtype)
     if workspace is None:
-        if dev.index == torch.cuda.current_device():
-            need = kv_attention_workspace(hq, h, d, max_new)
-        else:
-            with torch.cuda.device(dev):
-                need = kv_attention_workspace(hq, h, d, max_new)
-        workspace = _scratch(dev, stream, need, dtype=torch.uint8)
-    _call(dev, stream, "kq_kv_attention", qtype, _ptr(q), t, qs, hq, h, d, _ptr(cu_new), _ptr(seq_lens), n, int(max_new),
-          _ptr(k_pool), _ptr(v_pool), k_pool.shape[0], k_pool.shape[2], _ptr(block_table), block_table.shape[1],
-          d ** -0.5 if scale is None else scale, int(bool(causal)), int(window), _ptr(out), _ptr(workspace),
+        workspace = _scratch(k_pool, stream, _workspace_bytes(dev, hq, h, d, max_new), torch.uint8)
+    _call(dev, stream, "kq_kv_attention", qtype, q.data_ptr(), t, qs, hq, h, d, cu_new.data_ptr(), seq_lens.data_ptr(), n,
+          max_new, k_pool.data_ptr(), v_pool.data_ptr(), pages, page_size, block_table.data_ptr(), table[1],
+          d ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), workspace.data_ptr(),
           workspace.numel() * workspace.element_size(), _ptr(err))
     return out

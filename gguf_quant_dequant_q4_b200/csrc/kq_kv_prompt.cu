@@ -568,12 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
         uint32_t st = 0, par = 0, n = 0, seg = 0;
         const uint32_t sw = (row & 7) << 4;
         // tile number m into `base`, from the next raw tile; a key that is not
-        // there is zero, and so is a value block whose scale is not finite (its
-        // key is noted for the rows of segment vseg, before the tile is handed over)
-        bool vthere = false;
-        int vkey = 0;
-        uint32_t vseg = 0;
-        auto decode = [&](uint32_t base, uint64_t* full, uint64_t* empty, uint32_t m, bool there, bool value) {
+        // there is zero, and so is a block whose scale is not finite (its key is
+        // noted for the rows of segment sg, before the tile is handed over)
+        auto decode = [&](uint32_t base, uint64_t* full, uint64_t* empty, uint32_t m, bool there, int key, uint32_t sg) {
             bool ok = wait(&bar.raw_full[st], par);
             ok = wait(&empty[m & 1], ((m >> 1) & 1) ^ 1) && ok;
             ok = __all_sync(0xffffffffu, ok);
@@ -593,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                     uint32_t d = NB == 4 ? (b ? __byte_perm(x[4], x[4], 0x3232) : __byte_perm(x[0], x[0], 0x1010))
                                          : __byte_perm(x[0], x[0], odd ? 0x3232 : 0x1010);
                     if (!there) d = 0;
-                    if (value && (d & 0x7c00u) == 0x7c00u) {
+                    if ((d & 0x7c00u) == 0x7c00u) {
                         bad = true;
                         d = 0;
                     }
@@ -616,8 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                     }
                 }
                 if (bad) {
-                    atomicMin(&bad_lo[vseg & 7], vkey);
-                    atomicMax(&bad_hi[vseg & 7], vkey);
+                    atomicMin(&bad_lo[sg & 7], key);
+                    atomicMax(&bad_hi[sg & 7], key);
                 }
                 fence_proxy_async();
             }
@@ -631,8 +628,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                 par ^= 1;
             }
         };
-        bool pending = false;
-        auto values = [&]() { decode(sb + C::kV, bar.v_full, bar.v_empty, n - 1, vthere, true); };
+        bool pending = false, vthere = false;   // of the tile whose values come next
+        int vkey = 0;
+        uint32_t vseg = 0;
+        auto values = [&]() { decode(sb + C::kV, bar.v_full, bar.v_empty, n - 1, vthere, vkey, vseg); };
         while (left > 0) {
             const Span sp = span_of(p, s, at.rt);
             const Part pt = part_of(at, sp, left);
@@ -640,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                 const int key = (sp.t0 + pt.t0 + j) * kKeys + row;
                 wait(&bar.raw_full[st], par);   // the loader's mask is there with the raw tile
                 const bool there = key < s.len && key >= sp.lo && ((tmask[n & 15] >> (row >> 4)) & 1u);
-                decode(sb + C::kK, bar.k_full, bar.k_empty, n, there, false);
+                decode(sb + C::kK, bar.k_full, bar.k_empty, n, there, key, seg);
                 if (pending) values();
                 vthere = there;
                 vkey = key;
