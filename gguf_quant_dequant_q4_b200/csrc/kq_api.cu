@@ -338,8 +338,8 @@ int kq_kv_append(int type, const void* k, const void* v, int in_type, int64_t n_
     if (rc) return rc;
     if (in_type != KQ_F32 && in_type != KQ_BF16) return KQ_ERR_UNSUPPORTED;
     if (n_tokens < 0 || n_tokens > kMaxKvTokens) return KQ_ERR_INVALID_ARG;
-    // 64 blocks of 32 values a CTA, and the grid's x extent
-    if (n_tokens * n_kv_heads > (int64_t(1) << 31)) return KQ_ERR_INVALID_ARG;
+    // blocks are counted in 32 bits
+    if (n_tokens * n_kv_heads * (head_dim / 32) > kMaxK - 64) return KQ_ERR_INVALID_ARG;
     const int64_t row = static_cast<int64_t>(n_kv_heads) * head_dim;
     const int64_t per16 = in_type == KQ_F32 ? 4 : 8;
     if (k_stride < row || v_stride < row || k_stride > kMaxK || v_stride > kMaxK) return KQ_ERR_INVALID_ARG;

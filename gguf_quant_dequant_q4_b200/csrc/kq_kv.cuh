@@ -36,6 +36,25 @@ int launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, A.
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Division of n < 2^31 by a divisor known on the host: umulhi(n, mul) >> shift
+// with 2^k < d <= 2^(k + 1) (k = shift) and mul = ceil(2^(32 + k) / d) < 2^32:
+// mul d exceeds 2^(32 + k) by less than d, and n 2^(k + 1) < 2^(32 + k), so the
+// product's error stays below 1 / d.  d = 1 has mul 0.
+struct Divisor {
+    uint32_t mul;
+    int shift;
+};
+inline Divisor divisor_of(uint64_t d) {
+    Divisor r{0, 0};
+    if (d < 2) return r;
+    while ((uint64_t(2) << r.shift) < d) ++r.shift;
+    r.mul = static_cast<uint32_t>(((uint64_t(1) << (32 + r.shift)) + d - 1) / d);
+    return r;
+}
+__device__ __forceinline__ int divide(int n, const Divisor& d) {
+    return d.mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), d.mul) >> d.shift) : n;
+}
+
 // An attention call as its kernels take it.
 struct AttnParams {
     const uint16_t* q;
@@ -43,16 +62,13 @@ struct AttnParams {
     uint16_t* out;               // [n_tokens, n_heads, D]
     int n_tokens;
     int n_heads, n_kv, group;
-    uint32_t group_mul;          // division by the group size: see group_of
-    int group_shift;
+    Divisor by_group, by_page;
     const int32_t* cu;
     const int32_t* lens;
     int n_seqs;
     const uint8_t* kp;
     const uint8_t* vp;
     int n_pages, page;
-    uint32_t page_mul;           // division by the page size: see page_of
-    int page_shift;
     const int32_t* table;
     int max_blocks;
     float scale;                 // times log2(e)
@@ -64,11 +80,6 @@ struct AttnParams {
     int* status;
 };
 
-// Token of a row, floor(n / group) for n < 2^31: as page_of, with n 2^(k + 1) <
-// 2^(32 + k).
-__device__ __forceinline__ int group_of(const AttnParams& p, int n) {
-    return p.group == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), p.group_mul) >> p.group_shift);
-}
 // Bounded wait of a pipeline (all threads of a warp, or one): few instructions
 // while it lasts, so that warps that wait leave the issue slots to those that
 // work.  False once the limit has passed, or where another wait of the CTA has
@@ -87,13 +98,10 @@ __device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile
     if (status) atomicOr(status, KQ_DEV_TIMEOUT);
     return false;
 }
-// Table place of a key (a multiple of 16): floor(n / d) of n = key / 8 < 2^27
-// and d = page / 8 as umulhi(n, m) >> k with 2^k < d <= 2^(k + 1) and m =
-// ceil(2^(32 + k) / d) < 2^32: m d exceeds 2^(32 + k) by less than d, and n d <=
-// 2^27 2^(k + 1) < 2^(32 + k), so the product's error stays below 1 / d.
-__device__ __forceinline__ int page_of(const AttnParams& p, int key) {
-    return static_cast<int>(__umulhi(static_cast<uint32_t>(key) >> 3, p.page_mul) >> p.page_shift);
-}
+
+// Token of a row, table place of a key.
+__device__ __forceinline__ int group_of(const AttnParams& p, int row) { return divide(row, p.by_group); }
+__device__ __forceinline__ int page_of(const AttnParams& p, int key) { return divide(key, p.by_page); }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;

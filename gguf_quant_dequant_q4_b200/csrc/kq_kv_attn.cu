@@ -893,13 +893,6 @@ bool has_prompts(int head_dim, int max_new, int group) {
 
 }  // namespace
 
-// m = ceil(2^(32 + k) / d) with 2^k < d <= 2^(k + 1), for d >= 2.
-static void divide_by(uint64_t d, uint32_t& m, int& k) {
-    k = 0;
-    while ((uint64_t(2) << k) < d) ++k;
-    m = static_cast<uint32_t>(((uint64_t(1) << (32 + k)) + d - 1) / d);
-}
-
 int64_t kv_attention_workspace(int n_heads, int n_kv, int head_dim, int max_new) {
     const int r = rows_of(max_new, n_heads / n_kv);
     const int ctas = device_sm_count() * 2;
@@ -924,8 +917,8 @@ int launch_kv_attention(const KvAttention& a, cudaStream_t s) {
     p.vp = static_cast<const uint8_t*>(a.v_pool);
     p.n_pages = static_cast<int>(a.n_pages);
     p.page = a.page_size;
-    divide_by(static_cast<uint64_t>(a.page_size) / 8, p.page_mul, p.page_shift);
-    if (p.group > 1) divide_by(static_cast<uint64_t>(p.group), p.group_mul, p.group_shift);
+    p.by_page = divisor_of(static_cast<uint64_t>(a.page_size));
+    p.by_group = divisor_of(static_cast<uint64_t>(p.group));
     p.table = a.block_table;
     p.max_blocks = static_cast<int>(a.max_blocks);
     p.scale = a.scale * kLog2e;
