@@ -51,6 +51,12 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
 // A and B from shared memory.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -419,95 +425,103 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
     if (warp >= kMmaWarp) {
         regs_dec<56>();
         if (warp == kMmaWarp) {
-            if (lane == 0) {
-                // -------------------------------------------- MMA issuer
-                constexpr uint32_t iqk = idesc_of(kKeys, false), ipv = idesc_of(D, true);
-                uint32_t n = 0;                          // tiles so far
-                uint32_t hn[2] = {0, 0}, hs[2] = {0, 0};   // tiles and segments of each half (the second may be idle)
-                uint32_t hf[2] = {0, 0};                   // S given back
-                for (; left > 0;) {
-                    const Part pt = part_of(at, span_of(p, s, at.rt), left);
-                    const int tiles = pt.n;
-                    const int halves = tiles == 0 ? 0 : s.rows - at.rt * kRows > 128 ? 2 : 1;
-                    bool ok = true;
-                    for (int i = 0; i < halves; ++i) ok = ok && wait(&bar.q_full[i], hs[i] & 1);
-                    auto qk = [&](int i, uint32_t m) {   // S of half i = q K^T, tile number m
-                        const uint64_t a = sw128_desc(sb + C::kQ + i * C::kTileB, 16);
-                        const uint64_t b = sw128_desc(sb + C::kK + (m & 1) * C::kTileB, 16);
+            // ------------------------------------------------ MMA issuer
+            // The whole warp goes through the loop and one elected lane issues:
+            // operands that are the same in all lanes by construction (what was
+            // loaded comes through a shuffle) sit in uniform registers, where an
+            // instruction issued from one lane's own registers takes a loop of
+            // its own each time, about 100 cycles, longer than the MMA.
+            constexpr uint32_t iqk = idesc_of(kKeys, false), ipv = idesc_of(D, true);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint64_t qd = sw128_desc(sb + C::kQ, 16), kd = sw128_desc(sb + C::kK, 16), vd = sw128_desc(sb + C::kV, C::kHalfB);
+            uint32_t n = 0;                            // tiles so far
+            uint32_t hn[2] = {0, 0}, hs[2] = {0, 0};   // tiles and segments of each half (the second may be idle)
+            uint32_t hf[2] = {0, 0};                   // S given back
+            bool ok = true;
+            auto await = [&](uint64_t* b, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && wait(b, parity)); };
+            auto qk = [&](int i, uint32_t m) {   // S of half i = q K^T, tile number m
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t a = qd + (i * C::kTileB >> 4), b = kd + ((m & 1) * C::kTileB >> 4);
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t o = ((k >> 2) * C::kHalfB + (k & 3) * 32) >> 4;
-                            mma_ss(tmem + i * 128, a + o, b + o, iqk, k != 0);
-                        }
-                        tc_commit(&bar.s_full[i]);
-                    };
-                    // O of half i += P V, tile number m, as the two sides of P come in
-                    auto pv = [&](int i, uint32_t m, bool first) {
-                        const uint64_t b = sw128_desc(sb + C::kV + (m & 1) * C::kTileB, C::kHalfB);
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            if (!wait(&bar.p_full[2 * i + z], hn[i] & 1)) return false;
-                            tc_fence_after();
-#pragma unroll
-                            for (int k = 4 * z; k < 4 * z + 4; ++k)
-                                mma_ts(tmem + C::kO + i * D, tmem + C::kP + i * C::kPHalf + 8 * k, b + (k * 2048 >> 4), ipv,
-                                       !first || k != 0);
-                        }
-                        tc_commit(&bar.o_full[i]);
-                        return true;
-                    };
-                    if (tiles > 0) {
-                        ok = ok && wait(&bar.k_full[n & 1], (n >> 1) & 1);
-                        if (ok) {
-                            tc_fence_after();
-                            for (int i = 0; i < halves; ++i) qk(i, n);
-                            tc_commit(&bar.k_empty[n & 1]);
-                        }
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t o = ((k >> 2) * C::kHalfB + (k & 3) * 32) >> 4;
+                        mma_ss(tm + i * 128, a + o, b + o, iqk, k != 0);
                     }
-                    for (int j = 0; j < tiles; ++j, ++n) {
-                        const bool more = j + 1 < tiles;
-                        if constexpr (C::apart) {
-                            if (more) {
-                                ok = ok && wait(&bar.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
-                                for (int i = 0; i < halves; ++i) {
-                                    ok = ok && wait(&bar.s_free[i], hf[i] & 1);
-                                    if (!ok) break;
-                                    ++hf[i];
-                                    tc_fence_after();
-                                    qk(i, n + 1);
-                                }
-                                if (ok) tc_commit(&bar.k_empty[(n + 1) & 1]);
-                            }
-                        }
-                        ok = ok && wait(&bar.v_full[n & 1], (n >> 1) & 1);
-                        for (int i = 0; i < halves; ++i) {
-                            ok = ok && pv(i, n, j == 0);
-                            if constexpr (!C::apart) {
-                                // S shares its room with P: after P V in the same queue
-                                if (more) {
-                                    if (i == 0) ok = ok && wait(&bar.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
-                                    if (ok) {
-                                        tc_fence_after();
-                                        qk(i, n + 1);
-                                    }
-                                }
+                    tc_commit(&bar.s_full[i]);
+                }
+                __syncwarp();
+            };
+            // O of half i += P V, tile number m, as the two sides of P come in
+            auto pv = [&](int i, uint32_t m, bool first) {
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    await(&bar.p_full[2 * i + z], hn[i] & 1);
+                    if (!ok) return;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t b = vd + ((m & 1) * C::kTileB >> 4);
+#pragma unroll
+                        for (int k = 4 * z; k < 4 * z + 4; ++k)
+                            mma_ts(tm + C::kO + i * D, tm + C::kP + i * C::kPHalf + 8 * k, b + (k * 2048 >> 4), ipv,
+                                   !first || k != 0);
+                        if (z == 1) tc_commit(&bar.o_full[i]);
+                    }
+                    __syncwarp();
+                }
+            };
+            auto commit = [&](uint64_t* b) {
+                if (elect_one()) tc_commit(b);
+                __syncwarp();
+            };
+            while (left > 0 && ok) {
+                const Part pt = part_of(at, span_of(p, s, at.rt), left);
+                const int tiles = __shfl_sync(0xffffffffu, pt.n, 0);
+                const int halves = __shfl_sync(0xffffffffu, tiles == 0 ? 0 : s.rows - at.rt * kRows > 128 ? 2 : 1, 0);
+                for (int i = 0; i < halves; ++i) await(&bar.q_full[i], hs[i] & 1);
+                if (tiles > 0) {
+                    await(&bar.k_full[n & 1], (n >> 1) & 1);
+                    if (!ok) break;
+                    for (int i = 0; i < halves; ++i) qk(i, n);
+                    commit(&bar.k_empty[n & 1]);
+                }
+                for (int j = 0; j < tiles; ++j, ++n) {
+                    const bool more = j + 1 < tiles;
+                    if constexpr (C::apart) {
+                        if (more) {
+                            await(&bar.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
+                            for (int i = 0; i < halves; ++i) {
+                                await(&bar.s_free[i], hf[i] & 1);
+                                if (!ok) break;
+                                ++hf[i];
+                                qk(i, n + 1);
                             }
                             if (!ok) break;
-                            ++hn[i];
+                            commit(&bar.k_empty[(n + 1) & 1]);
                         }
-                        if (!ok) break;
-                        if (!C::apart && more) tc_commit(&bar.k_empty[(n + 1) & 1]);
-                        tc_commit(&bar.v_empty[n & 1]);
+                    }
+                    await(&bar.v_full[n & 1], (n >> 1) & 1);
+                    for (int i = 0; i < halves && ok; ++i) {
+                        pv(i, n, j == 0);
+                        if constexpr (!C::apart) {
+                            // S shares its room with P: after P V in the same queue
+                            if (more) {
+                                if (i == 0) await(&bar.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
+                                if (ok) qk(i, n + 1);
+                            }
+                        }
+                        ++hn[i];
                     }
                     if (!ok) break;
-                    for (int i = 0; i < halves; ++i) ++hs[i];
-                    left -= pt.units;
-                    if (left > 0) advance(p, at, s);
+                    if (!C::apart && more) commit(&bar.k_empty[(n + 1) & 1]);
+                    commit(&bar.v_empty[n & 1]);
                 }
-                // nothing of this CTA's may arrive after its end
-                if (n > 0) wait(&bar.v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1);
+                for (int i = 0; i < halves; ++i) ++hs[i];
+                left = __shfl_sync(0xffffffffu, left - pt.units, 0);
+                if (left > 0) advance(p, at, s);
             }
-            __syncwarp();
+            // nothing of this CTA's may arrive after its end
+            if (n > 0 && ok) wait(&bar.v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1);
         } else if (warp == kLoadWarp) {
             // ------------------------------------------------ loader
             // raw tiles in the order K0, then K(j+1), V(j), over the share
