@@ -543,7 +543,7 @@ def kv_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, qt
     if out is None:
         out = _scratch(q, stream, (t, hq, d), q.dtype)
     if workspace is None:
-        workspace = _scratch(k_pool, stream, _workspace_bytes(dev, hq, h, d, max_new), torch.uint8)
+        workspace = _scratch(k_pool, stream, _workspace_bytes(dev, hq, h, d, max(1, max_new)), torch.uint8)
     _call(dev, stream, "kq_kv_attention", qtype, q.data_ptr(), t, qs, hq, h, d, cu_new.data_ptr(), seq_lens.data_ptr(), n,
           max_new, k_pool.data_ptr(), v_pool.data_ptr(), pages, page_size, block_table.data_ptr(), table[1],
           d ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), workspace.data_ptr(),

@@ -54,9 +54,9 @@ int check_weights(int type, const void* w, int64_t n, int64_t k) {
     return KQ_OK;
 }
 
-// Limits of the KV-cache calls: tokens, table places and free pages are
-// counted in 32 bits with room for sums of two.
-constexpr int64_t kMaxKvTokens = int64_t(1) << 30;
+// Limit of the KV-cache calls: tokens, table places and free pages are counted
+// in 32 bits, with room for the sum of two and a page.
+constexpr int64_t kMaxKvTokens = (int64_t(1) << 30) - (int64_t(1) << 16);
 
 // A block table row of max_blocks pages.
 int check_table(int64_t page_size, int64_t max_blocks) {
@@ -376,9 +376,10 @@ int kq_kv_attention(int type, const uint16_t* q, int64_t n_tokens, int64_t q_str
     // the rows of one key head are counted in 32 bits
     if (n_tokens * (n_heads / n_kv_heads) > kMaxK - 256) return KQ_ERR_INVALID_ARG;
     const int64_t row = static_cast<int64_t>(n_heads) * head_dim;
-    if (q_stride < row || q_stride > kMaxK || max_new < 1 || window < 0 || window > kMaxKvTokens) return KQ_ERR_INVALID_ARG;
+    if (q_stride < row || q_stride > kMaxK || window < 0 || window > kMaxKvTokens) return KQ_ERR_INVALID_ARG;
     if (!(scale - scale == 0.f)) return KQ_ERR_INVALID_ARG;   // finite
     if (n_tokens == 0 || n_seqs == 0) return KQ_OK;
+    if (max_new < 1) return KQ_ERR_INVALID_ARG;
     if (!q || !cu_new || !seq_lens || !out || !workspace || (n_pages > 0 && (!k_pool || !v_pool)) ||
         (max_blocks > 0 && !block_table))
         return KQ_ERR_INVALID_ARG;

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
     pdl_launch();
     pdl_wait();
     const int part = threadIdx.x & 3;
-    const int i = static_cast<int>((blockIdx.x * 256u + threadIdx.x) >> 2);   // block
+    const int i = static_cast<int>(blockIdx.x * 64u + (threadIdx.x >> 2));   // block
     const bool in = i < p.n_blocks;
     const int row = (in ? i : 0) / NB, blk = (in ? i : 0) - row * NB;
     const int tok = divide(row, p.by_heads), head = row - tok * p.n_heads;

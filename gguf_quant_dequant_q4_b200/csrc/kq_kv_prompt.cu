@@ -88,31 +88,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* v) {
         : "r"(a)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld64(uint32_t a, uint32_t* v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, "
-        "%38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, "
-        "%60, %61, %62, %63}, [%64];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : KQ_R8(v, 0), KQ_R8(v, 8), KQ_R8(v, 16), KQ_R8(v, 24), KQ_R8(v, 32), KQ_R8(v, 40), KQ_R8(v, 48), KQ_R8(v, 56)
-        : "r"(a)
-        : "memory");
+__device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t* v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : KQ_R8(v, 0)
+                 : "r"(a)
+                 : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
-        KQ_I8(v, 0), KQ_I8(v, 8), KQ_I8(v, 16), KQ_I8(v, 24)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t* v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-        "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
-        : KQ_R8(v, 0), KQ_R8(v, 8)
-        : "r"(a)
-        : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a), KQ_I8(v, 0) : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t* v) {
     asm volatile(
@@ -351,10 +334,10 @@ struct Shape {
     static constexpr uint32_t kSmem = kRaw0 + kRaw * kRawB + 1024;
     static constexpr int kSlot = kRows * D + 2 * kRows;      // floats of a partial result
     // Tensor memory: S of both halves, O of both, and with 64-value heads P
-    // beside S, so that the next S is ready when a softmax ends; with 128 P
-    // takes the first half of its S.
+    // beside S, so that the next S is ready when a softmax ends; with 128 each
+    // side's P takes the first half of its S.
     static constexpr bool apart = NB == 2;
-    static constexpr uint32_t kO = 256, kP = apart ? 384 : 0, kPHalf = apart ? 64 : 128;
+    static constexpr uint32_t kO = 256, kP = apart ? 384 : 0, kPHalf = apart ? 64 : 128, kPSide = apart ? 32 : 64;
 };
 
 struct Bars {
@@ -463,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                         const uint64_t b = vd + ((m & 1) * C::kTileB >> 4);
 #pragma unroll
                         for (int k = 4 * z; k < 4 * z + 4; ++k)
-                            mma_ts(tm + C::kO + i * D, tm + C::kP + i * C::kPHalf + 8 * k, b + (k * 2048 >> 4), ipv,
+                            mma_ts(tm + C::kO + i * D, tm + C::kP + i * C::kPHalf + z * C::kPSide + 8 * (k - 4 * z), b + (k * 2048 >> 4), ipv,
                                    !first || k != 0);
                         if (z == 1) tc_commit(&bar.o_full[i]);
                     }
@@ -673,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
         const int half = warp >> 3, side = (warp >> 2) & 1, row = 32 * (warp & 3) + lane, pr = 128 * half + row;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // this warp's 32 lanes of tensor memory
         const uint32_t ts = tmem + half * 128 + 64 * side + lanes;
-        const uint32_t tp = tmem + C::kP + half * C::kPHalf + 32 * side + lanes;
+        const uint32_t tp = tmem + C::kP + half * C::kPHalf + side * C::kPSide + lanes;
         const uint32_t to = tmem + C::kO + half * D + D / 2 * side + lanes;
         // exchange with the row's other thread: double-buffered, so that one
         // barrier of the two warps is enough
@@ -768,19 +751,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                     wait(&bar.s_full[half], (hn + j) & 1);
                     __syncwarp();
                     tc_fence_after();
-                    uint32_t x[64];
-                    tmem_ld32(ts, x);
-                    tmem_ld32(ts + 32, x + 32);
-                    if (C::apart && j + 1 < tiles) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.s_free[half]);
-                    }
                     const int key0 = (sp.t0 + pt.t0 + j) * kKeys + 64 * side;
                     const uint32_t mask = (tmask[(n + j) & 15] >> (4 * side)) & 15u;
-                    if (key0 + 63 > all_hi || key0 < all_lo || mask != 15u) {
-#pragma unroll
-                        for (int w = 0; w < 2; ++w) {
+                    const bool edge = key0 + 63 > all_hi || key0 < all_lo || mask != 15u;
+                    // 32 keys of S at a time (keys 32 w ..), hidden ones -inf: the
+                    // second 32, then the first, which stay in registers, and the
+                    // second again after those are done
+                    uint32_t x[32];
+                    auto load = [&](int w) {
+                        tmem_ld32(ts + 32 * w, x);
+                        if (edge) {
                             // bits of the keys that this row sees
                             const int h0 = hi - key0 - 32 * w, l0 = lo - key0 - 32 * w;
                             uint32_t bits = h0 < 0 ? 0u : (h0 >= 31 ? ~0u : (2u << h0) - 1u);
@@ -788,20 +768,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                             bits &= ((mask >> (2 * w)) & 1u ? 0xffffu : 0u) | ((mask >> (2 * w)) & 2u ? 0xffff0000u : 0u);
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                if (!((bits >> k) & 1u)) x[32 * w + k] = 0xff800000u;
+                                if (!((bits >> k) & 1u)) x[k] = 0xff800000u;
                         }
-                    }
-                    float mx[4];     // (one chain would wait for each step)
+                    };
+                    auto largest = [&]() {
+                        float mx[4];     // (one chain would wait for each step)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 4]));
+                        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 4]));
 #pragma unroll
-                    for (int k = 8; k < 64; k += 8)
+                        for (int k = 8; k < 32; k += 8)
 #pragma unroll
-                        for (int z = 0; z < 4; ++z)
-                            mx[z] = fmaxf(mx[z], fmaxf(__uint_as_float(x[k + z]), __uint_as_float(x[k + z + 4])));
-                    float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                    // (the barrier also shows that both sides have read S, over
-                    // which P goes)
+                            for (int z = 0; z < 4; ++z)
+                                mx[z] = fmaxf(mx[z], fmaxf(__uint_as_float(x[k + z]), __uint_as_float(x[k + z + 4])));
+                        return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    };
+                    load(1);
+                    float mt = largest();
+                    load(0);
+                    mt = fmaxf(mt, largest()) * c;
                     mt = fmaxf(mt, other(mt));
                     // P V of the tile before is done with P and O
                     if (j > 0) wait(&bar.o_full[half], (hn + j - 1) & 1);
@@ -815,27 +799,37 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                         l2.y *= f;
                         if (j > 0) {
 #pragma unroll 1
-                            for (int k = 0; k < D / 32; ++k) {
-                                uint32_t o[16];
-                                tmem_ld16(to + 16 * k, o);
+                            for (int k = 0; k < D / 16; ++k) {
+                                uint32_t o[8];
+                                tmem_ld8(to + 8 * k, o);
 #pragma unroll
-                                for (int z = 0; z < 16; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
-                                tmem_st16(to + 16 * k, o);
+                                for (int z = 0; z < 8; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
+                                tmem_st8(to + 8 * k, o);
                             }
                         }
                     }
                     const float bias = m == -INFINITY ? 0.f : kPBias - m;
                     const float2 cc = make_float2(c, c), bb = make_float2(bias, bias);
+                    auto power = [&](int w) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        float2 y = make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
-                        y = fma2(y, cc, bb);
-                        y.x = ex2(y.x);
-                        y.y = ex2(y.y);
-                        l2 = add2(l2, y);
-                        x[k] = pack_f16x2(y.x, y.y);
+                        for (int k = 0; k < 16; ++k) {
+                            float2 y = make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+                            y = fma2(y, cc, bb);
+                            y.x = ex2(y.x);
+                            y.y = ex2(y.y);
+                            l2 = add2(l2, y);
+                            x[k] = pack_f16x2(y.x, y.y);
+                        }
+                        tmem_st16(tp + 16 * w, x);
+                    };
+                    power(0);
+                    load(1);
+                    if (C::apart && j + 1 < tiles) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.s_free[half]);
                     }
-                    tmem_st32(tp, x);
+                    power(1);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();

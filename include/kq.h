@@ -49,7 +49,8 @@
  *    blocks), and at most 2^31 - 1; otherwise KQ_ERR_INVALID_ARG.
  *  - Environment (read once per process; A/B levers, not needed in use):
  *    KQ_NO_PDL=1 launches the decode kernels (kq_qmv, kq_gather_qmv,
- *    kq_moe_glu_gather) without programmatic dependent launch, so a launch
+ *    kq_moe_glu_gather) and the KV-cache kernels without programmatic
+ *    dependent launch, so a launch
  *    no longer overlaps its start-up with the end of the previous kernel on
  *    the stream (the kernels and their results are unchanged);
  *    KQ_QMM_1SM=1 runs kq_qmm / kq_gather_qmm on single CTAs (128 weight
@@ -385,7 +386,7 @@ int kq_gather_mix(const float* y, int64_t rows, int64_t n, const int32_t* inv_or
  * but get slot -1 (and table entry -1).  Negative lengths count as 0, cached
  * lengths past the row are cut, pages below 0 or past 32-bit slots give slot
  * -1: KQ_DEV_BAD_RANGE.  n_seqs <= 2^20, cap, n_free and max_blocks *
- * page_size <= 2^30.
+ * page_size <= 2^30 - 2^16.
  */
 int kq_kv_plan(const int32_t* cached_lens, const int32_t* new_lens, int64_t n_seqs, int32_t page_size,
                int32_t* block_table, int64_t max_blocks, const int32_t* free_pages, int64_t n_free,
@@ -394,7 +395,8 @@ int kq_kv_plan(const int32_t* cached_lens, const int32_t* new_lens, int64_t n_se
 
 /*
  * kq_kv_append - encode the keys and values of n_tokens tokens into their
- * slots.
+ * slots.  n_tokens <= 2^30 - 2^16, n_tokens * n_kv_heads * head_dim / 32 < 2^31
+ * - 64.
  *   type        KQ_Q4_0 (else KQ_ERR_UNSUPPORTED)
  *   k, v        [n_tokens, n_kv_heads, head_dim] of in_type KQ_F32 (a product's
  *               output) or KQ_BF16; token rows k_stride, v_stride elements
@@ -426,8 +428,8 @@ int kq_kv_attention_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_
  *   cu_new      [n_seqs + 1] int32, seq_lens [n_seqs] int32 (device; as
  *               kq_kv_plan writes them): keys of sequence b, its own new
  *               tokens among them (append first)
- *   max_new     the largest number of new tokens of a sequence (host): chooses
- *               kernels, never the result's meaning
+ *   max_new     the largest number of new tokens of a sequence (host, >= 1 where
+ *               there are tokens): chooses kernels, never the result's meaning
  *   block_table [n_seqs, max_blocks]; a page outside [0, n_pages) that holds
  *               visible keys sets KQ_DEV_BAD_RANGE in err_flag (nullable) and
  *               its keys count as hidden
@@ -444,7 +446,11 @@ int kq_kv_attention_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_
  * Query head h reads key head h / (n_heads / n_kv_heads).  Scores, softmax
  * statistics and outputs are accumulated in fp32; probabilities are rounded to
  * binary16.  Deterministic (no atomics on data).  A non-finite q sets
- * KQ_DEV_X_RANGE.  n_tokens <= 2^30, n_seqs <= 2^20, window <= 2^30.
+ * KQ_DEV_X_RANGE.  A cached key or value whose block scale is not finite makes
+ * the rows that see it NaN (with many new tokens also rows that see keys on
+ * both sides of it); cached values past 65504 in magnitude (scales past 8188)
+ * count as such there.  n_tokens, window and max_blocks * page_size <= 2^30 -
+ * 2^16, n_seqs <= 2^20, n_tokens * n_heads / n_kv_heads < 2^31 - 256.
  */
 int kq_kv_attention(int type, const uint16_t* q, int64_t n_tokens, int64_t q_stride, int32_t n_heads,
                     int32_t n_kv_heads, int32_t head_dim, const int32_t* cu_new, const int32_t* seq_lens,
