@@ -319,7 +319,7 @@ __device__ __forceinline__ int encode_store(const float (&x)[8], bool put, bool 
             if (q == 3) w[4] = (bytes >> 16) | (next_d << 16);
         }
     }
-    return put && (hb & 0x7c00u) == 0x7c00u ? KQ_DEV_X_RANGE : 0;
+    return put && (hb & 0x7fffu) > 0x6fffu ? KQ_DEV_X_RANGE : 0;   // past 8188: a value past 65504
 }
 
 template <bool F32, int NB>

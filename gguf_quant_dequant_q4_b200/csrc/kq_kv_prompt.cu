@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
         uint32_t st = 0, par = 0, n = 0, seg = 0;
         const uint32_t sw = (row & 7) << 4;
         // tile number m into `base`, from the next raw tile; a key that is not
-        // there is zero, and so is a block whose scale is not finite (its key is
+        // there is zero, and so is a block whose scale passes 8188 (its key is
         // noted for the rows of segment sg, before the tile is handed over)
         auto decode = [&](uint32_t base, uint64_t* full, uint64_t* empty, uint32_t m, bool there, int key, uint32_t sg) {
             bool ok = wait(&bar.raw_full[st], par);
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                     uint32_t d = NB == 4 ? (b ? __byte_perm(x[4], x[4], 0x3232) : __byte_perm(x[0], x[0], 0x1010))
                                          : __byte_perm(x[0], x[0], odd ? 0x3232 : 0x1010);
                     if (!there) d = 0;
-                    if ((d & 0x7c00u) == 0x7c00u) {
+                    if ((d & 0x7fffu) > 0x6fffu) {   // past 8188: 8 d is no binary16 value
                         bad = true;
                         d = 0;
                     }

@@ -407,8 +407,9 @@ int kq_kv_plan(const int32_t* cached_lens, const int32_t* new_lens, int64_t n_se
  * Encoding, per block of 32 values, each step in fp32: d = -m / 8, m the value
  * of largest magnitude (the first of equals), stored as binary16; codes
  * min(15, trunc(x * (1 / d) + 8.5)); a block whose stored d is 0 has codes 8.
- * A block with a non-finite value, or whose d leaves binary16's range, stores
- * an infinite or NaN d and sets KQ_DEV_X_RANGE.  No other slot is touched.
+ * A block with a non-finite value or one whose magnitude passes 65504
+ * (binary16's range) sets KQ_DEV_X_RANGE and stores what the rule gives, an
+ * infinite or NaN d included.  No other slot is touched.
  */
 int kq_kv_append(int type, const void* k, const void* v, int in_type, int64_t n_tokens, int64_t k_stride,
                  int64_t v_stride, int32_t n_kv_heads, int32_t head_dim, const int32_t* slot_map, void* k_pool,

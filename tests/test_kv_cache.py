@@ -348,6 +348,15 @@ def test_append_flags():
         fine[1, 1, 32:] = False
         assert torch.equal(got[fine], torch.ones_like(got[fine])) and not torch.isfinite(got[1, 1, 40])
     err.zero_()
+    y = x.clone()
+    y[2, 0, 3] = -65504.0                        # the largest magnitude that is not flagged
+    kq.kv_append(x, y, kp, vp, kq.Q4_0, i32([0, 1, 2, 3]), err=err)
+    assert int(err) == 0
+    y[2, 0, 3] = 66000.0
+    kq.kv_append(x, y, kp, vp, kq.Q4_0, i32([0, 1, 2, 3]), err=err)
+    assert int(err) == kq.DEV_X_RANGE and float(kq.dequantize(vp, kq.Q4_0, 64)[0, 0, 2, 3]) > 57000
+    err.zero_()
+    y = x.clone()
     y[1, 1, 40] = float("nan")                   # not flagged where nothing is stored
     kq.kv_append(y, y, kp, vp, kq.Q4_0, i32([0, -1, 2, 3]), err=err)
     assert int(err) == 0
@@ -547,6 +556,26 @@ def test_values_that_are_not_numbers_stay_with_their_rows():
     fine = torch.ones(2, 4, dtype=torch.bool)
     fine[0, 1] = False
     assert torch.isfinite(got[fine.cuda()]).all()
+
+
+@gpu
+@pytest.mark.parametrize("pool", ["k", "v"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_keys_whose_scale_is_not_finite(pool, d):
+    # token 100 of 200: the rows that see it are not numbers, the others are
+    # what they are, on either side of it (a window of 30)
+    case = _kv.Case([(200, 200), (150, 90)], 2, 1, d, 16, seed=6)
+    want = case.expected(0.1, True, 30)
+    raw = case.k if pool == "k" else case.v
+    at = case.table[0, 100 // 16], 0, 100 % 16
+    for word in (0x7e, 0x7c, 0x71):                # NaN, infinite, 10240 and more
+        raw[at][19] = word
+        got = attend(case, 0.1, True, 30)
+        assert not torch.isfinite(got[100:130]).any()
+        fine = [i for i in range(290) if not 100 <= i < 130]
+        part = _kv.Case.__new__(_kv.Case)
+        part.expected = lambda *a: tuple(x[fine] for x in want)
+        check(part, got[fine], 0.1, wide=True)
 
 
 @gpu
