@@ -377,7 +377,8 @@ int kq_kv_attention(int type, const uint16_t* q, int64_t n_tokens, int64_t q_str
     if (n_tokens * (n_heads / n_kv_heads) > kMaxK - 256) return KQ_ERR_INVALID_ARG;
     const int64_t row = static_cast<int64_t>(n_heads) * head_dim;
     if (q_stride < row || q_stride > kMaxK || window < 0 || window > kMaxKvTokens) return KQ_ERR_INVALID_ARG;
-    if (!(scale - scale == 0.f)) return KQ_ERR_INVALID_ARG;   // finite
+    const float base2 = scale * 1.4426950408889634f;            // as the kernels take it
+    if (!(base2 - base2 == 0.f)) return KQ_ERR_INVALID_ARG;     // finite
     if (n_tokens == 0 || n_seqs == 0) return KQ_OK;
     if (max_new < 1) return KQ_ERR_INVALID_ARG;
     if (!q || !cu_new || !seq_lens || !out || !workspace || (n_pages > 0 && (!k_pool || !v_pool)) ||

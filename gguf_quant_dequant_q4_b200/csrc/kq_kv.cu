@@ -10,9 +10,15 @@
 // of that token writes the table entry, and every other thread of the page
 // computes the same page from free_pages without reading the table.
 //
+// Both are bound by latency (one launch for up to 4096 tokens, else two):
+// 48 requests of one token 4.0 us, 1021 prompts of 460,000 tokens 8.8 us.
+//
 // kq_kv_append writes each 32-value block as d = -m / 8 (m the value of
 // largest magnitude, the first of equals) and codes trunc(x * (1/d) + 8.5) in
 // 0..15, every step a separately rounded fp32 operation.
+// Bound by memory for prompts, by latency for a step: 8192 tokens of 8 heads of
+// 128 in fp32 19.1 us (77 MB, 4.0 TB/s), 2777 tokens of 5 heads of 64 in bf16
+// 8 us, 48 tokens of 8 heads of 128 in bf16 5.7 us.
 #include "kq_kv.cuh"
 
 namespace kq {

@@ -1,35 +1,49 @@
-// kq_kv_attention over a paged q4_0 cache, for steps of few tokens a sequence.
+// kq_kv_attention over a paged q4_0 cache, for steps of few tokens a sequence
+// (and every step whose head size the prompt kernel does not cover).
 //
 // One pass over the keys with a running maximum and sum: for the rows (token,
 // query head) that share one key head,
 //   o = sum_j 2^(y_j - m) v_j / sum_j 2^(y_j - m),  y_j = log2(e) scale q.k_j.
 // The wire blocks are never expanded to values.  The tensor cores take the
-// 4-bit codes as binary16 subnormals (code * 2^-24: two AND-masks turn four
-// packed codes into two operand words; mma.sync keeps subnormal operands
+// 4-bit codes as binary16 subnormals (mma.sync keeps subnormal operands
 // exact), keys as the rows of the A operand:
-//   S[key, row]  = sum over blocks of d(key, block) * ((code - 8) . q)   where
-//                  the -8 is the accumulator's start, -8 * sum of the block's q
-//   O[dim, row] += (code - 8)[dim, key] * (P d)[key, row]                 where
-//                  the -8 comes off at the end, as 8 sum P d in fp32.
+//   S[key, row]  = sum over blocks of d(key, block) * ((code - 8) . q): two
+//                  AND-masks turn four packed codes into two operand words, the
+//                  high ones 16 times too large, against q / 16; the -8 is the
+//                  accumulator's start, -8 * sum of the block's q
+//   O[dim, row] += code[dim, key] * (P d)[key, row]: the low codes, and whole
+//                  bytes (low + 16 high), from which the low sums come off at
+//                  the end, as does 8 sum P d
 // q is scaled by a power of two per row (as every decode kernel of this
 // library), so only P and P * d are rounded, to binary16, each by at most
-// 2^-11 of its value: P is held as 2^13 * P and d is divided by a power of
-// two near the largest |d| of the value rows seen so far, so that neither
-// the smallest P nor tiny or huge values leave binary16's range.  Maximum,
-// sum and both accumulators are fp32.
+// 2^-11 of its value: P enters as 2^5 P, with a reference that moves only when
+// the row's maximum is more than 2^8 above it, and d divided by a power of two
+// near the largest |d| of the value rows seen so far, so that neither small P
+// nor tiny or huge values leave binary16's range.  Maximum, sum and all
+// accumulators are fp32.
 //
 // Work is cut by keys, not by sequences: the tiles of 32 keys of all
 // (sequence, key head, 8 or 16 rows) segments form one list, and every CTA of
 // a grid that fills the GPU once takes an equal run of it, whatever the
 // lengths (found on the device from the lengths; the host reads nothing).  In
 // a CTA one warp reads the block table and issues bulk copies of 16- or
-// 32-key runs into a ring of stages; the other warps take the tiles in turn, each
-// with a maximum, sum and accumulator of its own, joined in shared memory at
-// the end of a segment.  A segment that spans CTAs leaves fp32 partial results
-// in the workspace, joined in list order by a second kernel: no atomics, the
-// same result on every run.
+// 32-key runs into a ring of stages; the other warps take the tiles in turn,
+// each with a maximum, sum and accumulator of its own, joined in shared memory
+// at the end of a segment.  A segment that spans CTAs leaves fp32 partial
+// results in the work space, joined in list order by a second kernel: no
+// atomics on data, the same result on every run.
 //
-// Bound by HBM: 0.5625 bytes per cached value.
+// Bound by instruction issue, close to HBM (0.5625 bytes a cached value):
+// one sequence of 700 keys, 32 heads over 8 of 128: 13.9 us; 24 of up to 4100
+// keys, 16 over 16 of 64: 31.5; 16 of up to 6000 with 3 to 5 tokens each and a
+// window, 16 over 4 of 256: 35.4; 48 of up to 8192, 32 over 8 of 128: 67 us
+// (3.3 TB/s); 2 of 150,000 to 200,000, 64 over 8 of 128: 95.6 us (4.2 TB/s).
+// What the steps were worth on the last of these: work split by keys 143 us;
+// four producer lanes a tile, value scales through a table 117; q in shared
+// memory, in-place rescaling, whole bytes 100; segments' fixed cost in the
+// split 96 (and 87 -> 67 on the ragged batch).  Fetching by the consumer warps
+// themselves instead of a producer: 115, more warps at fewer registers: 117 to
+// 133, -8 by exact subtraction from every operand: 117.
 #include "kq_kv.cuh"
 
 namespace kq {
@@ -38,7 +52,9 @@ namespace {
 constexpr int kTile = 32;        // keys of a tile
 // A segment counts as its tiles and kSegCost more in the list: its queries,
 // first copies and join take about as long as that many tiles.  A CTA whose
-// part of a segment is within these has nothing to do there.
+// part of a segment is within these has nothing to do there.  (Ragged batch of
+// 48 sequences up to 8192 keys: 87 us without, 70 with 12, 68 with 20, 70 with
+// 28, 78 with 60.)
 constexpr int kSegCost = 20;
 constexpr int kMinShare = kSegCost + 7;   // least units of a CTA's share: a tile a warp
 // P enters as 2^5 P, and a row's reference moves when its maximum is more than
@@ -101,8 +117,7 @@ __device__ __forceinline__ Part part_of(const Place& at, const Seq& s) {
     return r;
 }
 
-// Whole list length and the place of the unit at `share * blockIdx`, by the
-// threads of warp 0 .. all; results through shared memory.
+// Length of the list, by all threads of the CTA.
 template <int R>
 __device__ __forceinline__ int64_t list_total(const AttnParams& p, unsigned long long* sum) {
     if (threadIdx.x == 0) *sum = 0;
@@ -882,7 +897,9 @@ int launch_of(AttnParams p, cudaStream_t s) {
     return launch_pdl(attn_join_kernel<NB, NT>, dim3(static_cast<unsigned>(p.n_ctas - 1), NB / 2), 128, 0, s, p);
 }
 
-// Sequences with more rows a key head than this go to the prompt kernel.
+// Sequences with more rows a key head than this go to the prompt kernel.  64
+// rows: 16 sequences of 4000 keys 132 us here and 93 there, one of 8000 (48
+// rows) 28 here and 36 there, where 256-row tiles leave SMs idle.
 constexpr int kFew = 32;
 
 // Rows of a segment: 8 where a sequence's rows of one key head fit, else 16.

@@ -9,24 +9,43 @@
 // maximum m is only moved when a row's new one is more than 8 (a factor 2^8)
 // above it, so O is rescaled rarely; P stays below 2^15.
 //
-// Warp-specialized, one CTA an SM, 16 warps:
-//   warps 0..3, 4..7  softmax of rows 0..127 and 128..255 (thread = row): q into
-//                     shared memory, S from tensor memory, P back, the output
-//   warps 8..11       decoders: wire rows -> binary16 key and value tiles in the
-//                     128-byte-swizzled layout (thread = key; the tile of keys
-//                     is the K-major operand of Q K^T, the same layout of
-//                     values the MN-major operand of P V)
-//   warp 12           tcgen05.mma issuer and tensor memory allocator
-//   warp 13           block table and bulk copies of 16-key runs
+// Warp-specialized, one CTA an SM, 28 warps:
+//   warps 0..15   softmax, two threads a row: warps 0..7 rows 0..127 (first
+//                 half), 8..15 rows 128..255; in each the first four take keys
+//                 0..63 of a tile and the first half of q's and the output's
+//                 values, the others the rest.  q into shared memory, S from
+//                 tensor memory, P back, the output
+//   warps 16..23  decoders: wire rows -> binary16 key and value tiles in the
+//                 128-byte-swizzled layout (thread = key and half of its
+//                 blocks; the tile of keys is the K-major operand of Q K^T, the
+//                 same layout of values the MN-major operand of P V)
+//   warp 24       tcgen05.mma issuer and tensor memory allocator
+//   warp 25       block table and bulk copies of 16-key runs
 // The two halves alternate: while one half's softmax runs, the tensor cores
-// work on the other's P V and next Q K^T.  S and P share tensor memory: the
-// next Q K^T of a half is issued after its P V, and MMAs complete in order.
-// The order of the 32 values inside a block is whatever the code masks give;
-// q is stored in the same order and the output is put back in registers.
+// work on the other's P V and next Q K^T.  With 128-value heads S and P share
+// tensor memory, and the next Q K^T of a half is issued after its P V (MMAs
+// complete in order); with 64 there is room for both, and the next S is ready
+// when a softmax ends.  The order of the 32 values inside a block is whatever
+// the code masks give; q is stored in the same order and the output is put
+// back in registers.
 //
 // Work is the list of (sequence, key head, 256 rows, 128 keys) tiles that the
 // causal mask and window leave, cut into equal runs, one a CTA, as in the
-// few-row kernel; a segment that spans CTAs leaves fp32 partial results.
+// few-row kernel; a segment that spans CTAs leaves fp32 partial results.  The
+// runs' places are found once, by one CTA, not by every CTA.
+//
+// Bound by the chain of waits between softmax, MMA issue and tensor cores;
+// neither the tensor pipe (40 %) nor the exponentials (45 % with 64-value
+// heads) are full:
+// the last 2048 tokens of 8048, 32 heads over 8 of 128: 278 us (0.85 PFLOP/s);
+// ragged prompts of up to 2500 tokens and as many keys before them, 24 heads
+// over 8 of 64: 330 us (0.39 PFLOP/s).
+// What the steps were worth on the first of these: 16-row mma.sync tiles 2513
+// us; this kernel with one softmax thread a row 402; two threads a row and the
+// plan by one CTA 306; MMAs issued by an elected lane of a whole warp 286; S by
+// 32 keys, without spills, 278.  A cubic on the FMA pipe for 1/8 to 1/2 of the
+// exponentials: 306 to 342 for 306; the halves' start half a tile apart: 317
+// for 286.
 #include "kq_kv.cuh"
 
 namespace kq {
@@ -37,7 +56,8 @@ constexpr int kSoft = 16, kDec = 8;                 // warps: softmax, decoders
 constexpr int kMmaWarp = kSoft + kDec, kLoadWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kSoft + kDec + 4);   // seven warpgroups (two warps idle)
 // A segment counts as its tiles and kSegCost more in the list: its queries,
-// first tiles and output take about as long as that many tiles.
+// first tiles and output take about as long as that many tiles (ragged prompts:
+// 347 us with 2, 325 with 4, 335 with 6, 353 with 9).
 constexpr int kSegCost = 4;
 constexpr int kRaw = 3;            // raw tiles in flight
 constexpr int kMinShare = kSegCost + 3;   // least units of a CTA's share

@@ -91,6 +91,7 @@ def test_attention_refusals():
     assert call(window=-1) == INVALID
     assert call(scale=float("nan")) == INVALID
     assert call(scale=float("inf")) == INVALID
+    assert call(scale=3e38) == INVALID               # (infinite as a base-2 scale)
     assert call(page=8) == UNSUPPORTED
     assert call(blocks=2**40) == INVALID
     assert call(t=2**30 + 1) == INVALID
