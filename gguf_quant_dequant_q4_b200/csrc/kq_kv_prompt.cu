@@ -9,43 +9,47 @@
 // maximum m is only moved when a row's new one is more than 8 (a factor 2^8)
 // above it, so O is rescaled rarely; P stays below 2^15.
 //
-// Warp-specialized, one CTA an SM, 28 warps:
+// Warp-specialized, one CTA an SM, 28 warps (one idle):
 //   warps 0..15   softmax, two threads a row: warps 0..7 rows 0..127 (first
 //                 half), 8..15 rows 128..255; in each the first four take keys
-//                 0..63 of a tile and the first half of q's and the output's
-//                 values, the others the rest.  q into shared memory, S from
-//                 tensor memory, P back, the output
+//                 0..63 of every tile (first side), the others 64..127.  q into
+//                 shared memory, S from tensor memory, P back, the output
 //   warps 16..23  decoders: wire rows -> binary16 key and value tiles in the
 //                 128-byte-swizzled layout (thread = key and half of its
 //                 blocks; the tile of keys is the K-major operand of Q K^T, the
 //                 same layout of values the MN-major operand of P V)
-//   warp 24       tcgen05.mma issuer and tensor memory allocator
-//   warp 25       block table and bulk copies of 16-key runs
-// The two halves alternate: while one half's softmax runs, the tensor cores
-// work on the other's P V and next Q K^T.  With 128-value heads S and P share
-// tensor memory, and the next Q K^T of a half is issued after its P V (MMAs
-// complete in order); with 64 there is room for both, and the next S is ready
-// when a softmax ends.  The order of the 32 values inside a block is whatever
-// the code masks give; q is stored in the same order and the output is put
-// back in registers.
+//   warps 24, 25  tcgen05.mma issuers, one a half (the first also allocates
+//                 tensor memory): the tensor cores' queue holds a few MMAs, so
+//                 one warp's waits and loops run while the other's execute
+//   warp 26       block table and bulk copies of 16-key runs
+// A half's two sides take turns of 64 keys: S of both has its own 64 columns of
+// tensor memory, P takes the first 32 of them, and a side's next Q K^T is issued
+// after its P V (MMAs complete in order), while the other side computes.  All
+// four groups of four warps are apart, but for the row's reference m: each
+// side takes it over from the other's last 64 keys, and hands it on when it is
+// half through its exponentials, which keeps the sides out of step.  The order
+// of the 32 values inside a block is whatever the code masks give; q is stored
+// in the same order and the output is put back in registers.
 //
 // Work is the list of (sequence, key head, 256 rows, 128 keys) tiles that the
 // causal mask and window leave, cut into equal runs, one a CTA, as in the
 // few-row kernel; a segment that spans CTAs leaves fp32 partial results.  The
 // runs' places are found once, by one CTA, not by every CTA.
 //
-// Bound by the chain of waits between softmax, MMA issue and tensor cores;
-// neither the tensor pipe (40 %) nor the exponentials (45 % with 64-value
-// heads) are full:
-// the last 2048 tokens of 8048, 32 heads over 8 of 128: 278 us (0.85 PFLOP/s);
-// ragged prompts of up to 2500 tokens and as many keys before them, 24 heads
-// over 8 of 64: 330 us (0.39 PFLOP/s).
+// Bound by the chain of waits of a side (S, softmax, P, its MMAs); neither the
+// tensor pipe nor the exponentials (each about half of the time) are full:
+// the last 2048 tokens of 8048, 32 heads over 8 of 128: 255 us (0.92 PFLOP/s);
+// ragged prompts of up to 2500 tokens and as many as 1500 keys before them, 24
+// heads over 8 of 64: 290 us (0.45 PFLOP/s).
 // What the steps were worth on the first of these: 16-row mma.sync tiles 2513
 // us; this kernel with one softmax thread a row 402; two threads a row and the
 // plan by one CTA 306; MMAs issued by an elected lane of a whole warp 286; S by
-// 32 keys, without spills, 278.  A cubic on the FMA pipe for 1/8 to 1/2 of the
-// exponentials: 306 to 342 for 306; the halves' start half a tile apart: 317
-// for 286.
+// 32 keys, without spills, 278; 64 keys a side and one issuing warp 335, with
+// two 279; the reference handed over in one look 267; handed on half way and
+// fewer polls 255.  A cubic on the FMA pipe for 1/4 of the exponentials: 288
+// for 266; a side's 64 keys in registers at once: 292 for 266; Q K^T of both
+// sides at once: 340 for 279 (64 keys cost 51 cycles an MMA, 128 67, but the
+// sides wait for each other); polls without a pause: 302 for 266.
 #include "kq_kv.cuh"
 
 namespace kq {
@@ -53,8 +57,8 @@ namespace {
 
 constexpr int kRows = 256, kKeys = 128;
 constexpr int kSoft = 16, kDec = 8;                 // warps: softmax, decoders
-constexpr int kMmaWarp = kSoft + kDec, kLoadWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kSoft + kDec + 4);   // seven warpgroups (two warps idle)
+constexpr int kMmaWarp = kSoft + kDec, kLoadWarp = kMmaWarp + 2;
+constexpr int kThreads = 32 * (kSoft + kDec + 4);   // seven warpgroups (one warp idle)
 // A segment counts as its tiles and kSegCost more in the list: its queries,
 // first tiles and output take about as long as that many tiles (ragged prompts:
 // 347 us with 2, 325 with 4, 335 with 6, 353 with 9).
@@ -350,19 +354,18 @@ struct Shape {
     static constexpr uint32_t kHalfB = kKeys * 128;          // its first 64 values
     static constexpr uint32_t kRawB = kKeys * RB;
     static constexpr uint32_t kEx = 1024;                    // exchange between the two sides of a row
-    static constexpr uint32_t kQ = kEx + 4 * kRows * 4, kK = kQ + 2 * kTileB, kV = kK + 2 * kTileB, kRaw0 = kV + 2 * kTileB;
+    static constexpr uint32_t kQ = kEx + 5 * kRows * 4, kK = kQ + 2 * kTileB, kV = kK + 2 * kTileB, kRaw0 = kV + 2 * kTileB;
     static constexpr uint32_t kSmem = kRaw0 + kRaw * kRawB + 1024;
     static constexpr int kSlot = kRows * D + 2 * kRows;      // floats of a partial result
-    // Tensor memory: S of both halves, O of both, and with 64-value heads P
-    // beside S, so that the next S is ready when a softmax ends; with 128 each
-    // side's P takes the first half of its S.
-    static constexpr bool apart = NB == 2;
-    static constexpr uint32_t kO = 256, kP = apart ? 384 : 0, kPHalf = apart ? 64 : 128, kPSide = apart ? 32 : 64;
+    // Tensor memory: S of both halves and sides (64 columns each, P takes the
+    // first 32), O of both halves.
+    static constexpr uint32_t kO = 256;
 };
 
 struct Bars {
     uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t s_full[2], s_free[2], p_full[4], o_full[2], q_full[2];
+    uint64_t s_full[4], p_full[4], o_full[4], q_full[2];   // [2 half + side]
+    uint64_t m_full[16];                                   // [softmax warp]
 };
 
 template <int NB>
@@ -389,16 +392,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.k_full[i], kDec);
-            mbar_init(&bar.k_empty[i], 1);
+            mbar_init(&bar.k_empty[i], 2);
             mbar_init(&bar.v_full[i], kDec);
-            mbar_init(&bar.v_empty[i], 1);
-            mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.s_free[i], 8);
-            mbar_init(&bar.p_full[i], 4);
-            mbar_init(&bar.p_full[i + 2], 4);
-            mbar_init(&bar.o_full[i], 1);
+            mbar_init(&bar.v_empty[i], 2);
             mbar_init(&bar.q_full[i], 8);
         }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.p_full[i], 4);
+            mbar_init(&bar.o_full[i], 1);
+        }
+        for (int i = 0; i < 16; ++i) mbar_init(&bar.m_full[i], 1);
         for (int i = 0; i < 8; ++i) {
             bad_lo[i] = 0x7fffffff;
             bad_hi[i] = -1;
@@ -427,99 +431,81 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
 
     if (warp >= kMmaWarp) {
         regs_dec<56>();
-        if (warp == kMmaWarp) {
-            // ------------------------------------------------ MMA issuer
+        if (warp < kLoadWarp) {
+            // ------------------------------------------------ MMA issuers
             // The whole warp goes through the loop and one elected lane issues:
             // operands that are the same in all lanes by construction (what was
             // loaded comes through a shuffle) sit in uniform registers, where an
             // instruction issued from one lane's own registers takes a loop of
             // its own each time, about 100 cycles, longer than the MMA.
-            constexpr uint32_t iqk = idesc_of(kKeys, false), ipv = idesc_of(D, true);
-            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint64_t qd = sw128_desc(sb + C::kQ, 16), kd = sw128_desc(sb + C::kK, 16), vd = sw128_desc(sb + C::kV, C::kHalfB);
-            uint32_t n = 0;                            // tiles so far
-            uint32_t hn[2] = {0, 0}, hs[2] = {0, 0};   // tiles and segments of each half (the second may be idle)
-            uint32_t hf[2] = {0, 0};                   // S given back
+            constexpr uint32_t iqk = idesc_of(kKeys / 2, false), ipv = idesc_of(D, true);
+            const int i = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);   // half
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), ts = tm + i * 128, to = tm + C::kO + i * D;
+            const uint64_t qd = sw128_desc(sb + C::kQ + i * C::kTileB, 16), kd = sw128_desc(sb + C::kK, 16),
+                           vd = sw128_desc(sb + C::kV, C::kHalfB);
+            uint32_t n = 0;           // tiles so far
+            uint32_t hn = 0, hs = 0;  // tiles and segments of this half (the second may be idle)
             bool ok = true;
             auto await = [&](uint64_t* b, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && wait(b, parity)); };
-            auto qk = [&](int i, uint32_t m) {   // S of half i = q K^T, tile number m
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t a = qd + (i * C::kTileB >> 4), b = kd + ((m & 1) * C::kTileB >> 4);
+            auto qk = [&](int z, uint32_t m) {   // S of side z = q K^T, tile number m
+                const uint64_t b = kd + (((m & 1) * C::kTileB + z * 64 * 128) >> 4);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t o = ((k >> 2) * C::kHalfB + (k & 3) * 32) >> 4;
-                        mma_ss(tm + i * 128, a + o, b + o, iqk, k != 0);
-                    }
-                    tc_commit(&bar.s_full[i]);
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t o = ((k >> 2) * C::kHalfB + (k & 3) * 32) >> 4;
+                    mma_ss(ts + z * 64, qd + o, b + o, iqk, k != 0);
                 }
-                __syncwarp();
-            };
-            // O of half i += P V, tile number m, as the two sides of P come in
-            auto pv = [&](int i, uint32_t m, bool first) {
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    await(&bar.p_full[2 * i + z], hn[i] & 1);
-                    if (!ok) return;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t b = vd + ((m & 1) * C::kTileB >> 4);
-#pragma unroll
-                        for (int k = 4 * z; k < 4 * z + 4; ++k)
-                            mma_ts(tm + C::kO + i * D, tm + C::kP + i * C::kPHalf + z * C::kPSide + 8 * (k - 4 * z), b + (k * 2048 >> 4), ipv,
-                                   !first || k != 0);
-                        if (z == 1) tc_commit(&bar.o_full[i]);
-                    }
-                    __syncwarp();
-                }
-            };
-            auto commit = [&](uint64_t* b) {
-                if (elect_one()) tc_commit(b);
-                __syncwarp();
+                tc_commit(&bar.s_full[2 * i + z]);
             };
             while (left > 0 && ok) {
                 const Part pt = part_of(at, span_of(p, s, at.rt), left);
                 const int tiles = __shfl_sync(0xffffffffu, pt.n, 0);
-                const int halves = __shfl_sync(0xffffffffu, tiles == 0 ? 0 : s.rows - at.rt * kRows > 128 ? 2 : 1, 0);
-                for (int i = 0; i < halves; ++i) await(&bar.q_full[i], hs[i] & 1);
+                const bool used = __shfl_sync(0xffffffffu, tiles > 0 && (i == 0 || s.rows - at.rt * kRows > 128), 0);
+                if (used) {
+                    await(&bar.q_full[i], hs & 1);
+                    ++hs;
+                }
                 if (tiles > 0) {
                     await(&bar.k_full[n & 1], (n >> 1) & 1);
                     if (!ok) break;
-                    for (int i = 0; i < halves; ++i) qk(i, n);
-                    commit(&bar.k_empty[n & 1]);
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (used) {
+                            qk(0, n);
+                            qk(1, n);
+                        }
+                        tc_commit(&bar.k_empty[n & 1]);
+                    }
+                    __syncwarp();
                 }
                 for (int j = 0; j < tiles; ++j, ++n) {
                     const bool more = j + 1 < tiles;
-                    if constexpr (C::apart) {
-                        if (more) {
-                            await(&bar.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
-                            for (int i = 0; i < halves; ++i) {
-                                await(&bar.s_free[i], hf[i] & 1);
-                                if (!ok) break;
-                                ++hf[i];
-                                qk(i, n + 1);
-                            }
-                            if (!ok) break;
-                            commit(&bar.k_empty[(n + 1) & 1]);
-                        }
-                    }
                     await(&bar.v_full[n & 1], (n >> 1) & 1);
-                    for (int i = 0; i < halves && ok; ++i) {
-                        pv(i, n, j == 0);
-                        if constexpr (!C::apart) {
-                            // S shares its room with P: after P V in the same queue
-                            if (more) {
-                                if (i == 0) await(&bar.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
-                                if (ok) qk(i, n + 1);
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        if (used) await(&bar.p_full[2 * i + z], hn & 1);
+                        if (more && z == 0) await(&bar.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            if (used) {
+                                // O += P V of this side
+                                const uint64_t b = vd + (((n & 1) * C::kTileB + 4 * z * 2048) >> 4);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) mma_ts(to, ts + z * 64 + 8 * k, b + (k * 2048 >> 4), ipv, j > 0 || z != 0 || k != 0);
+                                tc_commit(&bar.o_full[2 * i + z]);
+                                // S shares its room with P: after P V in the same queue
+                                if (more) qk(z, n + 1);
+                            }
+                            if (z == 1) {
+                                if (more) tc_commit(&bar.k_empty[(n + 1) & 1]);
+                                tc_commit(&bar.v_empty[n & 1]);
                             }
                         }
-                        ++hn[i];
+                        __syncwarp();
                     }
                     if (!ok) break;
-                    if (!C::apart && more) commit(&bar.k_empty[(n + 1) & 1]);
-                    commit(&bar.v_empty[n & 1]);
+                    if (used) ++hn;
                 }
-                for (int i = 0; i < halves; ++i) ++hs[i];
                 left = __shfl_sync(0xffffffffu, left - pt.units, 0);
                 if (left > 0) advance(p, at, s);
             }
@@ -676,13 +662,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
         const int half = warp >> 3, side = (warp >> 2) & 1, row = 32 * (warp & 3) + lane, pr = 128 * half + row;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // this warp's 32 lanes of tensor memory
         const uint32_t ts = tmem + half * 128 + 64 * side + lanes;
-        const uint32_t tp = tmem + C::kP + half * C::kPHalf + side * C::kPSide + lanes;
-        const uint32_t to = tmem + C::kO + half * D + D / 2 * side + lanes;
+        const uint32_t to = tmem + C::kO + half * D + lanes;
         // exchange with the row's other thread: double-buffered, so that one
         // barrier of the two warps is enough
         float* ex = reinterpret_cast<float*>(smem + C::kEx) + pr;
         uint32_t flip = 0;
         const int pair = 1 + 4 * half + (warp & 3);
+        // the reference that the row's two threads hand each other: one word,
+        // written by whichever has its turn
+        float* mex = reinterpret_cast<float*>(smem + C::kEx) + 4 * kRows + pr;
+        uint64_t *mine = &bar.m_full[warp], *theirs = &bar.m_full[warp ^ 4];
         auto other = [&](float v) {
             ex[(flip + side) * kRows] = v;
             asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
@@ -765,10 +754,25 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                 }
                 float m = -INFINITY;     // reference of the exponents, times c
                 float2 l2 = make_float2(0.f, 0.f);
+                if (!side) *mex = m;
+                // moves the sum to another reference; the factor
+                auto follow = [&](float nm) {
+                    const float f = m == nm ? 1.f : ex2(m - nm);
+                    m = nm;
+                    l2.x *= f;
+                    l2.y *= f;
+                    return f;
+                };
                 for (int j = 0; j < tiles; ++j) {
                     // (where a wait has run out the CTA goes through its barriers all
                     // the same, on whatever is there)
-                    wait(&bar.s_full[half], (hn + j) & 1);
+                    wait(&bar.s_full[2 * half + side], (hn + j) & 1);
+                    // the reference after the 64 keys before these
+                    float before = m;
+                    if (side || j > 0) {
+                        wait(theirs, (hn + j - (side ^ 1)) & 1);
+                        before = *mex;
+                    }
                     __syncwarp();
                     tc_fence_after();
                     const int key0 = (sp.t0 + pt.t0 + j) * kKeys + 64 * side;
@@ -806,20 +810,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                     float mt = largest();
                     load(0);
                     mt = fmaxf(mt, largest()) * c;
-                    mt = fmaxf(mt, other(mt));
-                    // P V of the tile before is done with P and O
-                    if (j > 0) wait(&bar.o_full[half], (hn + j - 1) & 1);
-                    __syncwarp();
-                    tc_fence_after();
-                    if (__any_sync(0xffffffffu, mt > m + kLazy)) {
-                        const float nm = fmaxf(m, mt);
-                        const float f = m == nm ? 1.f : ex2(m - nm);
-                        m = nm;
-                        l2.x *= f;
-                        l2.y *= f;
-                        if (j > 0) {
+                    if (__any_sync(0xffffffffu, before != m || mt > before + kLazy)) {
+                        follow(before);
+                        const bool grow = __any_sync(0xffffffffu, mt > m + kLazy);
+                        const float nm = grow ? fmaxf(m, mt) : m;
+                        *mex = nm;
+                        const float f = follow(nm);
+                        if (grow && (side || j > 0)) {
+                            // O is the sum up to those keys once their P V is done
+                            wait(&bar.o_full[2 * half + (side ^ 1)], (hn + j - (side ^ 1)) & 1);
+                            __syncwarp();
+                            tc_fence_after();
 #pragma unroll 1
-                            for (int k = 0; k < D / 16; ++k) {
+                            for (int k = 0; k < D / 8; ++k) {
                                 uint32_t o[8];
                                 tmem_ld8(to + 8 * k, o);
 #pragma unroll
@@ -840,15 +843,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                             l2 = add2(l2, y);
                             x[k] = pack_f16x2(y.x, y.y);
                         }
-                        tmem_st16(tp + 16 * w, x);
+                        tmem_st16(ts + 16 * w, x);
                     };
                     power(0);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(mine);
                     load(1);
-                    if (C::apart && j + 1 < tiles) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.s_free[half]);
-                    }
                     power(1);
                     tmem_wait_st();
                     tc_fence_before();
@@ -856,9 +856,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                     if (lane == 0) mbar_arrive(&bar.p_full[2 * half + side]);
                 }
                 // ---- output
+                if (!side) {
+                    wait(theirs, (hn + tiles - 1) & 1);
+                    follow(*mex);
+                }
                 float l = l2.x + l2.y;
                 l += other(l);
-                if (__all_sync(0xffffffffu, wait(&bar.o_full[half], (hn + tiles - 1) & 1))) {
+                if (__all_sync(0xffffffffu, wait(&bar.o_full[2 * half + 1], (hn + tiles - 1) & 1))) {
                     tc_fence_after();
                     // a row that sees a key whose value scale is not finite
                     if (bad_hi[seg & 7] >= lo && bad_lo[seg & 7] <= hi && there) l = __int_as_float(0x7fc00000);
@@ -868,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
 #pragma unroll
                     for (int b = 0; b < HB; ++b) {
                         uint32_t o[32];
-                        tmem_ld32(to + 32 * b, o);
+                        tmem_ld32(to + D / 2 * side + 32 * b, o);
                         auto at_value = [&](int v) {   // value v of the block, from its place in the codes' order
                             float r = 0.f;
 #pragma unroll

@@ -480,6 +480,22 @@ def test_prompt_ranges(k_exp, v_exp, q_scale, scale):
 
 
 @gpu
+@pytest.mark.parametrize("slope", [0.08, 0.4, 3.0])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("seqs", [[(700, 300), (300, 140)], [(900, 1), (130, 2)]])
+def test_scores_that_rise_or_fall(seqs, d, slope):
+    # every key's score is `slope` above (even heads) or below (odd heads) the
+    # one before: the reference moves with every few keys, or never
+    case = _kv.Case(seqs, 4, 2, d, 16, seed=15)
+    for b, (n, _) in enumerate(seqs):
+        for j in range(n):
+            case.k[case.table[b, j // 16], :, j % 16] = _kv.encode(np.full((2, d), -j / 128, np.float32))
+    case.q = (torch.tensor([-1.0, 1.0, -1.0, 1.0])[:, None] * torch.ones_like(case.q)).to(torch.bfloat16)
+    scale = slope * 128 / d
+    check(case, attend(case, scale), scale, wide=True)
+
+
+@gpu
 def test_rows_that_see_nothing_and_rows_of_no_sequence():
     # a sequence without keys, and one with more new tokens than keys: zeros;
     # the padded rows behind the last sequence stay as they were
