@@ -11,6 +11,10 @@ Codecs (ggml type ids): ``Q4_0 = 2``, ``Q8_0 = 8``, ``Q4_K = 12``, ``Q5_K = 13``
 ``Q6_K = 14`` (q5_K and q4_0: dequantize and the tensor-core products).  Weights are
 wire bytes ``uint8 [N, row_bytes]`` ("transpose=True" layout: y = x @ W.T),
 activations ``bfloat16 [M, K]``, outputs ``float32``.
+
+KV cache (``kv_plan``, ``kv_append``, ``kv_attention``): pools of keys and of
+values are ``uint8 [pages, kv_heads, page_size, row_bytes(Q4_0, head_dim)]``, rows
+of q4_0 blocks as ``dequantize`` reads them.
 """
 from __future__ import annotations
 

@@ -16,8 +16,9 @@
 // kq_kv_append writes each 32-value block as d = -m / 8 (m the value of
 // largest magnitude, the first of equals) and codes trunc(x * (1/d) + 8.5) in
 // 0..15, every step a separately rounded fp32 operation.
-// Bound by memory for prompts, by latency for a step: 8192 tokens of 8 heads of
-// 128 in fp32 19.1 us (77 MB, 4.0 TB/s), 2777 tokens of 5 heads of 64 in bf16
+// Bound by instruction issue for prompts (72 % of the slots, the ALU pipe 68 %),
+// by latency for a step: 8192 tokens of 8 heads of 128 in fp32 19.1 us (77 MB,
+// 4.0 TB/s; packed fp32 multiplies and adds: 2 % less), 2777 tokens of 5 heads of 64 in bf16
 // 8 us, 48 tokens of 8 heads of 128 in bf16 5.7 us.
 #include "kq_kv.cuh"
 
@@ -232,8 +233,8 @@ struct AppendParams {
 };
 
 // Four lanes a block of 32 values, eight consecutive values a lane, for the key
-// and the value of the same place.  Bound by memory: 4 or 8 bytes read and
-// 1.125 written for a key and value.  An even block and the odd one after it
+// and the value of the same place: 4 or 8 bytes read and 1.125 written for a
+// key and value.  An even block and the odd one after it
 // are 9 words:
 //   d0 c0 c1 | c2..c5 | c6..c9 | c10..c13 | c14 c15 d1 | c0..c3 | ... | c12..c15
 // (c: code bytes), so the lanes of an even block store their four bytes shifted

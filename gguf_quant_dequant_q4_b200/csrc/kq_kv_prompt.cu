@@ -61,7 +61,7 @@ constexpr int kMmaWarp = kSoft + kDec, kLoadWarp = kMmaWarp + 2;
 constexpr int kThreads = 32 * (kSoft + kDec + 4);   // seven warpgroups (one warp idle)
 // A segment counts as its tiles and kSegCost more in the list: its queries,
 // first tiles and output take about as long as that many tiles (ragged prompts:
-// 347 us with 2, 325 with 4, 335 with 6, 353 with 9).
+// 304 us with 3, 290 with 4 or 5, 293 with 6).
 constexpr int kSegCost = 4;
 constexpr int kRaw = 3;            // raw tiles in flight
 constexpr int kMinShare = kSegCost + 3;   // least units of a CTA's share
