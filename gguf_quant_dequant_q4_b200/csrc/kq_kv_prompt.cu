@@ -49,7 +49,8 @@
 // fewer polls 255.  A cubic on the FMA pipe for 1/4 of the exponentials: 288
 // for 266; a side's 64 keys in registers at once: 292 for 266; Q K^T of both
 // sides at once: 340 for 279 (64 keys cost 51 cycles an MMA, 128 67, but the
-// sides wait for each other); polls without a pause: 302 for 266.
+// sides wait for each other); polls without a pause: 302 for 266; P beside S
+// with 64-value heads, the next Q K^T under the softmax: ragged 309 for 290.
 #include "kq_kv.cuh"
 
 namespace kq {
