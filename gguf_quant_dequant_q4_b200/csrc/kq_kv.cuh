@@ -97,6 +97,28 @@ __device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile
     return false;
 }
 
+// Rows and keys of sequence b.  Its tokens keep the places that the given
+// lengths say, whatever the tokens and the table row hold: the one at tok0 + i
+// stands at pos0 + i, and keys behind the row count as hidden.
+struct Given {
+    int tok0, qlen, pos0, len;   // first token, tokens, its position, keys that the table row holds
+    int bad;                     // KQ_DEV_* of lengths that do not fit
+};
+__device__ __forceinline__ Given given_of(const AttnParams& p, int b) {
+    Given s;
+    const int c0 = p.cu[b], c1 = p.cu[b + 1];
+    const int end = c1 < 0 ? 0 : (c1 > p.n_tokens ? p.n_tokens : c1);
+    s.tok0 = c0 < 0 ? 0 : (c0 > end ? end : c0);
+    s.qlen = end - s.tok0;
+    const int len = p.lens[b] < 0 ? 0 : p.lens[b], most = p.max_blocks * p.page;
+    s.len = len < most ? len : most;
+    // (positions below -qlen see as little as -qlen)
+    const int64_t pos = static_cast<int64_t>(len) - c1 + s.tok0;
+    s.pos0 = pos < -s.qlen ? -s.qlen : static_cast<int>(pos);
+    s.bad = (c0 < 0 || c1 > p.n_tokens || c1 < c0 ? KQ_DEV_BAD_RANGE : 0) | (len > most && s.qlen > 0 ? KQ_DEV_TOO_MANY : 0);
+    return s;
+}
+
 // Token of a row, table place of a key.
 __device__ __forceinline__ int group_of(const AttnParams& p, int row) { return divide(row, p.by_group); }
 __device__ __forceinline__ int page_of(const AttnParams& p, int key) { return divide(key, p.by_page); }

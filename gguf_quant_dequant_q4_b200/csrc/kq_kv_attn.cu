@@ -63,7 +63,7 @@ constexpr float kPBias = 5.f, kLazy = 8.f;
 
 // A sequence's share of the work.
 struct Seq {
-    int tok0, qlen, len;         // first token, tokens, keys
+    int tok0, qlen, pos0, len;   // first token, tokens, its position, keys
     int lo;                      // first key any row sees
     int t0, nt;                  // first tile, tiles of a segment
     int rt;                      // row tiles
@@ -71,24 +71,20 @@ struct Seq {
 
 template <int R>
 __device__ __forceinline__ Seq seq_of(const AttnParams& p, int b) {
+    const Given in = given_of(p, b);
     Seq s;
-    int c0 = p.cu[b], c1 = p.cu[b + 1];
-    c0 = c0 < 0 ? 0 : (c0 > p.n_tokens ? p.n_tokens : c0);
-    c1 = c1 < c0 ? c0 : (c1 > p.n_tokens ? p.n_tokens : c1);
-    s.tok0 = c0;
-    s.qlen = c1 - c0;
-    int len = p.lens[b];
-    const int most = p.max_blocks * p.page;
-    len = len < 0 ? 0 : (len > most ? most : len);
-    s.len = len;
+    s.tok0 = in.tok0;
+    s.qlen = in.qlen;
+    s.pos0 = in.pos0;
+    s.len = in.len;
     int lo = 0;
     if (p.window > 0) {
-        lo = len - s.qlen - p.window + 1;
-        lo = lo < 0 ? 0 : (lo > len ? len : lo);
+        lo = s.pos0 - p.window + 1;
+        lo = lo < 0 ? 0 : (lo > s.len ? s.len : lo);
     }
     s.lo = lo;
     s.t0 = lo / kTile;
-    const int nt = (len + kTile - 1) / kTile - s.t0;
+    const int nt = (s.len + kTile - 1) / kTile - s.t0;
     s.nt = nt < 1 ? 1 : nt;      // a segment without keys still writes its zeros
     const int rows = s.qlen * p.group;
     s.rt = rows > p.few ? 0 : (rows + R - 1) / R;   // (more rows: the prompt kernel's)
@@ -240,6 +236,11 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
     pdl_launch();
     pdl_wait();
     const int64_t total = list_total<R>(p, sum);
+    if (blockIdx.x == 0 && p.err) {   // (for the prompt kernel's sequences too)
+        int bad = 0;
+        for (int b = tid; b < p.n_seqs; b += C::kThreads) bad |= given_of(p, b).bad;
+        if (bad) atomicOr(p.err, bad);
+    }
     const int64_t share = share_of(total, p.n_ctas);
     const int64_t u0 = share * blockIdx.x;
     if (u0 >= total) return;
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
             if (t == 0) {
                 // 2^24 of the codes and 2^-e of the row, in two steps (e reaches 126)
                 yrow[r] = p.scale == 0.f ? 1.f : fmaxf(fabsf(p.scale) * 16777216.f * exp2_int(-e), 1.17549435e-38f);
-                const int pos = s.len - s.qlen + i;
+                const int pos = s.pos0 + i;
                 hirow[r] = p.causal ? min(pos, s.len - 1) : s.len - 1;
                 lorow[r] = p.window > 0 ? pos - p.window + 1 : 0;
             }
@@ -472,9 +473,9 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
             yscale[nt][1] = yrow[nt * 8 + 2 * t + 1];
         }
         // keys that every row of the segment sees
-        const int pos0 = s.len - s.qlen + (at.rt * R) / p.group;
+        const int pos0 = s.pos0 + (at.rt * R) / p.group;
         const int last_row = min(at.rt * R + R, s.qlen * p.group) - 1;
-        const int pos1 = s.len - s.qlen + last_row / p.group;
+        const int pos1 = s.pos0 + last_row / p.group;
         const int all_hi = p.causal ? min(pos0, s.len - 1) : s.len - 1;
         const int all_lo = p.window > 0 ? pos1 - p.window + 1 : 0;
 

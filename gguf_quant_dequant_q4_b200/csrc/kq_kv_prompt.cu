@@ -184,18 +184,15 @@ __device__ __forceinline__ constexpr int value_of(int b, int i, int e) {
 }
 
 struct Seq {
-    int tok0, qlen, len, rows;
+    int tok0, qlen, pos0, len, rows;
 };
 __device__ __forceinline__ Seq seq_of(const AttnParams& p, int b) {
+    const Given in = given_of(p, b);
     Seq s;
-    int c0 = p.cu[b], c1 = p.cu[b + 1];
-    c0 = c0 < 0 ? 0 : (c0 > p.n_tokens ? p.n_tokens : c0);
-    c1 = c1 < c0 ? c0 : (c1 > p.n_tokens ? p.n_tokens : c1);
-    s.tok0 = c0;
-    s.qlen = c1 - c0;
-    int len = p.lens[b];
-    const int most = p.max_blocks * p.page;
-    s.len = len < 0 ? 0 : (len > most ? most : len);
+    s.tok0 = in.tok0;
+    s.qlen = in.qlen;
+    s.pos0 = in.pos0;
+    s.len = in.len;
     s.rows = s.qlen * p.group;
     return s;
 }
@@ -205,9 +202,9 @@ struct Span {
     int t0, n, lo;
 };
 __device__ __forceinline__ Span span_of(const AttnParams& p, const Seq& s, int rt) {
-    const int first = s.len - s.qlen + group_of(p, rt * kRows);
+    const int first = s.pos0 + group_of(p, rt * kRows);
     const int end = min(rt * kRows + kRows, s.rows) - 1;
-    const int last = s.len - s.qlen + group_of(p, end);
+    const int last = s.pos0 + group_of(p, end);
     int hi = p.causal ? last + 1 : s.len;     // one past the last key
     hi = hi < 0 ? 0 : (hi > s.len ? s.len : hi);
     int lo = p.window > 0 ? first - p.window + 1 : 0;
@@ -694,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                 const bool there = rr < s.rows;
                 const int ti = there ? group_of(p, rr) : 0;
                 const int64_t qhead = static_cast<int64_t>(at.h) * p.group + (there ? rr - ti * p.group : 0);
-                const int pos = s.len - s.qlen + ti;
+                const int pos = s.pos0 + ti;
                 int hi = p.causal ? min(pos, s.len - 1) : s.len - 1;
                 int lo = p.window > 0 ? pos - p.window + 1 : 0;
                 if (!there) {

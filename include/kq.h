@@ -94,7 +94,7 @@ typedef enum {
 #define KQ_DEV_BAD_RANGE    0x4   /* tile rows past `rows`, count > cap        */
 #define KQ_DEV_UNSORTED     0x8   /* expert ids not ascending                  */
 #define KQ_DEV_TIMEOUT      0x10  /* a bounded pipeline wait ran out            */
-#define KQ_DEV_TOO_MANY     0x20  /* reserved: not set by this version         */
+#define KQ_DEV_TOO_MANY     0x20  /* KV cache: tokens past a limit of the call  */
 #define KQ_DEV_X_RANGE      0x40  /* an activation is infinite or NaN         */
 
 /* Block geometry of a codec (host only).  Returns KQ_OK or
@@ -428,7 +428,12 @@ int kq_kv_attention_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_
  *               cu_new[b + 1] - 1 are the last ones of sequence b
  *   cu_new      [n_seqs + 1] int32, seq_lens [n_seqs] int32 (device; as
  *               kq_kv_plan writes them): keys of sequence b, its own new
- *               tokens among them (append first)
+ *               tokens among them (append first).  Where a sequence with new
+ *               tokens is longer than its table row (max_blocks * page_size),
+ *               positions stay those of the given length, the keys past the row
+ *               count as hidden and KQ_DEV_TOO_MANY is set; offsets outside
+ *               [0, n_tokens] or that fall set KQ_DEV_BAD_RANGE, and the tokens
+ *               that are there keep their positions
  *   max_new     the largest number of new tokens of a sequence (host, >= 1 where
  *               there are tokens): chooses kernels, never the result's meaning
  *   block_table [n_seqs, max_blocks]; a page outside [0, n_pages) that holds

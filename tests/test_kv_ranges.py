@@ -1,0 +1,82 @@
+"""KV cache: lengths past a table row, large scores, values of very different
+magnitudes, scales out of range and slots named twice, against the plain forms
+of _kv.py."""
+import numpy as np
+import pytest
+import torch
+
+import gguf_quant_dequant_q4_b200 as kq
+from tests import _kv
+from tests.test_kv_cache import attend, check, flag, i32
+
+pytestmark = pytest.mark.gpu
+
+
+def rows_of(want, rows):
+    """A stand-in for a case whose expected values are some rows of `want`."""
+    part = _kv.Case.__new__(_kv.Case)
+    part.expected = lambda *a: tuple(x[rows] for x in want)
+    return part
+
+
+# ------------------------------------------------- lengths past the table row
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [4, 12, 60])   # few rows a key head, and prompts
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 20), (False, 0), (False, 20)])
+def test_lengths_past_the_table_row(d, new, causal, window):
+    # 140 tokens where the row holds 128: positions are those of the given
+    # length, and the keys behind the row count as hidden
+    case = _kv.Case([(100, 3), (140, new), (0, 0), (139, 1)], 4, 2, d, 16, seed=21)
+    want = case.expected(0.1, causal, window, [(1, 8), (3, 8)])
+    case.table = np.ascontiguousarray(case.table[:, :8])
+    err = flag()
+    got = attend(case, 0.1, causal, window, err=err)
+    check(rows_of(want, slice(None)), got, 0.1, wide=True)
+    assert int(err) == kq.DEV_TOO_MANY
+    # an idle request that is too long is nobody's concern
+    case.cu = np.array([0, 3, 3, 3, 3], np.int32)
+    err.zero_()
+    check(rows_of(want, slice(0, 3)), attend(case, 0.1, causal, window, err=err)[:3], 0.1)
+    assert int(err) == 0
+
+
+@pytest.mark.parametrize("d", [64, 192])
+@pytest.mark.parametrize("new", [10, 100])
+def test_offsets_past_the_tokens(d, new):
+    # q holds three tokens less than the offsets say: the others keep their places
+    case = _kv.Case([(40, 5), (300, new)], 4, 2, d, 16, seed=22)
+    want = case.expected(0.1, True, 50)
+    err = flag()
+    got = attend(case, 0.1, True, 50, q=case.q[:-3].cuda(), err=err)
+    check(rows_of(want, slice(0, 2 + new)), got, 0.1, wide=True)
+    assert int(err) == kq.DEV_BAD_RANGE
+
+
+@pytest.mark.parametrize("hq,d", [(4, 64), (8, 128), (4, 256)])
+def test_a_request_that_outgrows_its_row(hq, d):
+    """plan, append and attention: 20 cached and 20 new tokens in a row of two
+    16-token pages, beside a request that fits."""
+    page, hkv, rng = 16, 2, np.random.default_rng(d)
+    kp = torch.full((8, hkv, page, d // 32 * 18), 255, dtype=torch.uint8, device="cuda")
+    vp = kp.clone()
+    free, taken, table, err = i32(rng.permutation(8)), i32([0]), i32(np.full((2, 2), -1)), flag()
+    lens = i32([0, 0])
+    for step, new in enumerate(([20, 9], [20, 7])):
+        lens, cu, slots, pos = kq.kv_plan(lens, i32(new), table, free, taken, page, sum(new), err=err)
+        k, v = (torch.from_numpy(rng.standard_normal((sum(new), hkv, d)).astype(np.float32)).cuda() for _ in range(2))
+        kq.kv_append(k, v, kp, vp, kq.Q4_0, slots, err=err)
+        assert int(err) == (kq.DEV_TOO_MANY if step else 0)
+    assert lens.tolist() == [40, 16] and pos[:20].tolist() == list(range(20, 40))
+    assert slots[12:20].tolist() == [-1] * 8 and (slots[:12] >= 0).all()
+    case = _kv.Case.__new__(_kv.Case)
+    case.seqs, case.hq, case.hkv, case.d, case.page = [(40, 20), (16, 7)], hq, hkv, d, page
+    tab = table.cpu().numpy()
+    case.table = np.concatenate([tab, tab[:, :1]], 1)           # (the third page does not count)
+    case.lens, case.cu = np.array([40, 16]), np.array([0, 20, 27])
+    case.k, case.v = kp.cpu().numpy(), vp.cpu().numpy()
+    case.q = torch.from_numpy(rng.standard_normal((27, hq, d)).astype(np.float32)).to(torch.bfloat16)
+    want = case.expected(0.1, True, 0, [(0, 2)])
+    err.zero_()
+    got = kq.kv_attention(case.q.cuda(), kp, vp, kq.Q4_0, table, lens, cu, 20, scale=0.1, err=err)
+    check(rows_of(want, slice(None)), got, 0.1, wide=True)
+    assert int(err) == kq.DEV_TOO_MANY
