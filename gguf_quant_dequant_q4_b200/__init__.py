@@ -484,7 +484,8 @@ _PLAIN = {torch.float32: 0, torch.bfloat16: 30}  # ggml type ids of plain values
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, qtype: int,
               slot_map: torch.Tensor, err: torch.Tensor | None = None, stream=None) -> None:
     """Encode k, v [tokens, kv_heads, head_dim] (float32 or bfloat16; views of a
-    fused product's columns are fine) into the pools' slots; slot -1: left out."""
+    fused product's columns are fine) into the pools' slots; slot -1: left out.
+    A slot named by several tokens holds a mixture of their bytes."""
     if k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError(f"k and v must have one shape and type, got {tuple(k.shape)} {k.dtype}, {tuple(v.shape)} {v.dtype}")
     kind = _PLAIN.get(k.dtype)

@@ -239,7 +239,8 @@ struct AppendParams {
 //   d0 c0 c1 | c2..c5 | c6..c9 | c10..c13 | c14 c15 d1 | c0..c3 | ... | c12..c15
 // (c: code bytes), so the lanes of an even block store their four bytes shifted
 // by two, with the last two bytes of the lane before; those of an odd block as
-// they are.
+// they are.  Nothing orders the words of two tokens with one slot: each word is
+// one token's.
 template <bool F32>
 struct Eight {
     uint4 a, b;

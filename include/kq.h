@@ -402,8 +402,11 @@ int kq_kv_plan(const int32_t* cached_lens, const int32_t* new_lens, int64_t n_se
  *               output) or KQ_BF16; token rows k_stride, v_stride elements
  *               apart (>= n_kv_heads * head_dim, a multiple of 16 bytes)
  *   slot_map    [n_tokens] int32: -1 leaves the token out; other slots outside
- *               the pool are left out and flagged KQ_DEV_BAD_RANGE.  Where two
- *               tokens have one slot, each of its blocks holds one of the two.
+ *               the pool are left out and flagged KQ_DEV_BAD_RANGE.  Slots are
+ *               meant to differ: one that several tokens name ends up with a
+ *               mixture of their bytes (a block's scale may be one token's, its
+ *               codes another's); every other slot is unaffected
+ *   k_pool, v_pool  two pools that do not overlap
  * Encoding, per block of 32 values, each step in fp32: d = -m / 8, m the value
  * of largest magnitude (the first of equals), stored as binary16; codes
  * min(15, trunc(x * (1 / d) + 8.5)); a block whose stored d is 0 has codes 8.

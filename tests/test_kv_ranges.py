@@ -80,3 +80,26 @@ def test_a_request_that_outgrows_its_row(hq, d):
     got = kq.kv_attention(case.q.cuda(), kp, vp, kq.Q4_0, table, lens, cu, 20, scale=0.1, err=err)
     check(rows_of(want, slice(None)), got, 0.1, wide=True)
     assert int(err) == kq.DEV_TOO_MANY
+
+
+# -------------------------------------------------------- slots named twice
+@pytest.mark.parametrize("h,d,t", [(1, 64, 8), (2, 64, 700), (8, 128, 300), (3, 256, 64)])
+def test_slots_named_twice(h, d, t):
+    # which token's bytes such a slot holds is open, but they are the tokens'
+    # own, and every other slot is what it is
+    page, rng = 16, np.random.default_rng(t)
+    n_pages = 2 * t // page + 2
+    slots = rng.permutation(n_pages * page)[:t].astype(np.int32)
+    twice = slots[: t // 4].copy()
+    slots[t - t // 4:] = twice                     # the last quarter goes where the first went
+    k, v = (torch.from_numpy(rng.standard_normal((t, h, d)).astype(np.float32)) for _ in range(2))
+    pools = [torch.full((n_pages, h, page, d // 32 * 18), 9, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    kq.kv_append(k.cuda(), v.cuda(), pools[0], pools[1], kq.Q4_0, i32(slots))
+    for x, pool in ((k, pools[0]), (v, pools[1])):
+        rows, got = _kv.encode(x.numpy()), pool.transpose(1, 2).cpu().numpy().reshape(n_pages * page, h, -1)
+        once = slots[t // 4:t - t // 4]
+        np.testing.assert_array_equal(got[once], rows[t // 4:t - t // 4])
+        a, b = rows[: t // 4], rows[t - t // 4:]
+        assert ((got[twice] == a) | (got[twice] == b)).all()
+        rest = np.setdiff1d(np.arange(n_pages * page), slots)
+        assert (got[rest] == 9).all()
