@@ -16,8 +16,8 @@
 //                  the end, as does 8 sum P d
 // q is scaled by a power of two per row (as every decode kernel of this
 // library), so only P and P * d are rounded, to binary16, each by at most
-// 2^-11 of its value: P enters as 2^5 P, with a reference that moves only when
-// the row's maximum is more than 2^8 above it, and d divided by a power of two
+// 2^-11 of its value: P is relative to a reference 5 below the row's maximum,
+// which moves only when the maximum is more than 13 above it, and d is divided by a power of two
 // near the largest |d| of the value rows seen so far, so that neither small P
 // nor tiny or huge values leave binary16's range.  Maximum, sum and all
 // accumulators are fp32.
@@ -57,8 +57,9 @@ constexpr int kTile = 32;        // keys of a tile
 // 28, 78 with 60.)
 constexpr int kSegCost = 20;
 constexpr int kMinShare = kSegCost + 7;   // least units of a CTA's share: a tile a warp
-// P enters as 2^5 P, and a row's reference moves when its maximum is more than
-// 2^8 above it: P stays below 2^13, P * d below 2^15.
+// A row's reference is 5 below its maximum when it moves, which it does when the
+// maximum is more than 13 above it: P, 2^(score - reference), stays within 2^13,
+// P * d below 2^15.
 constexpr float kPBias = 5.f, kLazy = 8.f;
 
 // A sequence's share of the work.
@@ -552,6 +553,15 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
                     }
                 }
             }
+            // base-2 scores, rounded before the reference comes off them: were the
+            // exact product inside one FMA with a rounded reference, the largest
+            // P would be off by a power of two once scores pass 2^24 or so
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[j][nt][k] = __fmul_rn(y[j][nt][k], yscale[nt][k & 1]);
             const bool edge = there != 0xffffffffu || key0 + kTile - 1 > all_hi || key0 < all_lo;
             if (edge) {
 #pragma unroll
@@ -597,7 +607,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
                             if (((who >> tau(j, g + 8 * (k >> 1))) & 1u) && y[j][nt][k] != -INFINITY)
                                 l[nt][k & 1] = __int_as_float(0x7fc00000);
             }
-            // ---- running maximum, value exponent
+            // ---- reference (kPBias below a maximum), value exponent
             int ne = static_cast<int>(dmx >> 10) - 15;
             ne = ne > 14 ? 14 : ne;
             bool grow = ne > ve + 1;
@@ -610,8 +620,8 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    mt[nt][c] = fmaxf(m[nt][c], v * yscale[nt][c]);
-                    grow |= mt[nt][c] > m[nt][c] + kLazy;
+                    mt[nt][c] = fmaxf(m[nt][c], v - kPBias);
+                    grow |= v - m[nt][c] > kPBias + kLazy;   // (a difference of near values is exact)
                 }
             if (__any_sync(0xffffffffu, grow)) {
                 const int e = ne > ve ? ne : ve;
@@ -647,19 +657,19 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
                     sts_u16(scale_at + 64 * b + 64, two >> 16);
                 }
             }
-            // ---- P (2^5 P, binary16), transposed into B operand words
+            // ---- P (binary16), transposed into B operand words
             uint32_t pb[2][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float mm[2];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) mm[c] = m[nt][c] == -INFINITY ? 0.f : kPBias - m[nt][c];   // (all hidden: 2^-inf)
+                for (int c = 0; c < 2; ++c) mm[c] = m[nt][c] == -INFINITY ? 0.f : m[nt][c];   // (all hidden: 2^-inf)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     float e[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        e[k] = ex2(fmaf(y[j][nt][k], yscale[nt][k & 1], mm[k & 1]));
+                        e[k] = ex2(y[j][nt][k] - mm[k & 1]);
                         l[nt][k & 1] += e[k];
                     }
                     pb[j][nt][0] = movm(pack_f16x2(e[0], e[1]));

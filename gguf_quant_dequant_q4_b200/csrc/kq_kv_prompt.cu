@@ -4,10 +4,10 @@
 // Rows are (token, query head of the key head's group) pairs, so one key head's
 // tile is decoded once for 256 rows.  Keys and values become binary16 values
 // (code - 8) * d in shared memory (one rounding, 2^-11), S = Q K^T and O += P V
-// accumulate in fp32 in tensor memory, P = 2^7 * 2^(y - m) goes back to tensor
-// memory as binary16 and is the second product's A operand.  The running
-// maximum m is only moved when a row's new one is more than 8 (a factor 2^8)
-// above it, so O is rescaled rarely; P stays below 2^15.
+// accumulate in fp32 in tensor memory, P = 2^(y - m) goes back to tensor
+// memory as binary16 and is the second product's A operand.  The reference m,
+// 7 below the running maximum, is only moved when a row's new maximum is more
+// than 15 above it, so O is rescaled rarely; P stays below 2^15.1.
 //
 // Warp-specialized, one CTA an SM, 28 warps (one idle):
 //   warps 0..15   softmax, two threads a row: warps 0..7 rows 0..127 (first
@@ -66,7 +66,13 @@ constexpr int kThreads = 32 * (kSoft + kDec + 4);   // seven warpgroups (one war
 constexpr int kSegCost = 4;
 constexpr int kRaw = 3;            // raw tiles in flight
 constexpr int kMinShare = kSegCost + 3;   // least units of a CTA's share
+// A row's reference is 7 below its maximum when it moves, which it does when the
+// maximum is more than 15 above it.
 constexpr float kPBias = 7.f, kLazy = 8.f;
+// Exponents are one FMA of an exact product and the reference while |reference|
+// is within this, so that the reference's own rounding is at most 2^-4; past it
+// the products are rounded first, as the maximum is, or P could leave binary16.
+constexpr float kFar = 1048576.f;
 
 // ---------------------------------------------------------------- PTX glue
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -750,9 +756,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.q_full[half]);
                 }
-                float m = -INFINITY;     // reference of the exponents, times c
+                float m = -INFINITY;     // reference of the base-2 exponents
+                bool far = false;        // a reference of this warp's has been past kFar:
+                float cf = c;            // S is multiplied when it is loaded, and cf is 1
                 float2 l2 = make_float2(0.f, 0.f);
                 if (!side) *mex = m;
+                auto times = [](uint32_t a, float f) { return __float_as_uint(__fmul_rn(__uint_as_float(a), f)); };
                 // moves the sum to another reference; the factor
                 auto follow = [&](float nm) {
                     const float f = m == nm ? 1.f : ex2(m - nm);
@@ -775,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                     tc_fence_after();
                     const int key0 = (sp.t0 + pt.t0 + j) * kKeys + 64 * side;
                     const uint32_t mask = (tmask[(n + j) & 15] >> (4 * side)) & 15u;
-                    const bool edge = key0 + 63 > all_hi || key0 < all_lo || mask != 15u;
+                    bool edge = key0 + 63 > all_hi || key0 < all_lo || mask != 15u || far;
                     // 32 keys of S at a time (keys 32 w ..), hidden ones -inf: the
                     // second 32, then the first, which stay in registers, and the
                     // second again after those are done
@@ -791,6 +800,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
                                 if (!((bits >> k) & 1u)) x[k] = 0xff800000u;
+                            if (far) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) x[k] = times(x[k], c);
+                            }
                         }
                     };
                     auto largest = [&]() {
@@ -807,13 +820,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                     load(1);
                     float mt = largest();
                     load(0);
-                    mt = fmaxf(mt, largest()) * c;
-                    if (__any_sync(0xffffffffu, before != m || mt > before + kLazy)) {
+                    mt = __fmul_rn(fmaxf(mt, largest()), cf);
+                    if (__any_sync(0xffffffffu, before != m || mt - before > kPBias + kLazy)) {
                         follow(before);
-                        const bool grow = __any_sync(0xffffffffu, mt > m + kLazy);
-                        const float nm = grow ? fmaxf(m, mt) : m;
+                        const bool grow = __any_sync(0xffffffffu, mt - m > kPBias + kLazy);
+                        const float nm = grow ? fmaxf(m, mt - kPBias) : m;
                         *mex = nm;
                         const float f = follow(nm);
+                        if (!far && __any_sync(0xffffffffu, fabsf(m) > kFar && m != -INFINITY)) {
+                            far = edge = true;
+                            cf = 1.f;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) x[k] = times(x[k], c);
+                        }
                         if (grow && (side || j > 0)) {
                             // O is the sum up to those keys once their P V is done
                             wait(&bar.o_full[2 * half + (side ^ 1)], (hn + j - (side ^ 1)) & 1);
@@ -829,8 +848,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                             }
                         }
                     }
-                    const float bias = m == -INFINITY ? 0.f : kPBias - m;
-                    const float2 cc = make_float2(c, c), bb = make_float2(bias, bias);
+                    const float bias = m == -INFINITY ? 0.f : -m;
+                    const float2 cc = make_float2(cf, cf), bb = make_float2(bias, bias);
                     auto power = [&](int w) {
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {

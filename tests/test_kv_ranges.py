@@ -103,3 +103,36 @@ def test_slots_named_twice(h, d, t):
         assert ((got[twice] == a) | (got[twice] == b)).all()
         rest = np.setdiff1d(np.arange(n_pages * page), slots)
         assert (got[rest] == 9).all()
+
+
+# ------------------------------------------------------------- large scores
+def steep(seqs, d, q, kdiv):
+    """Key j of every sequence is -(j + 1) / kdiv in all of its values and q is
+    -1 (even heads) or 1 (odd heads) in all of its: scores are exact, the last
+    visible key (or the first) has the largest, by far."""
+    case = _kv.Case(seqs, 4, 2, d, 16, seed=23)
+    for b, (n, _) in enumerate(seqs):
+        for j in range(n):
+            case.k[case.table[b, j // 16], :, j % 16] = _kv.encode(np.full((2, d), -(j + 1) / kdiv, np.float32))
+    case.q = (torch.tensor([-q, q, -q, q])[:, None] * torch.ones(case.q.shape)).to(torch.bfloat16)
+    return case
+
+
+def check_steep(case, scale):
+    # one key has weight 1: P is a power of two, and what is left of check()'s
+    # bound are the roundings of P d or a decoded value, and of the output
+    want, mag, _, step = case.expected(scale)
+    got = attend(case, scale).double().cpu().numpy()
+    assert np.isfinite(got).all()
+    tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -10 + 2.0 ** -18) * mag * 1.02 + 2.0 ** -17 * step + 1e-30
+    assert (np.abs(got - want) / tol).max() <= 1.0
+
+
+STEEP = [[(70, 1), (300, 2)], [(200, 3), (33, 16)], [(400, 150), (90, 40)]]
+
+
+@pytest.mark.parametrize("q", [1e5, 1e6, 1e7, 3e8, 1e9, 1e10, 1e12, 1e20, 1e30])
+@pytest.mark.parametrize("seqs", STEEP)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_large_scores(seqs, d, q):
+    check_steep(steep(seqs, d, q, 128), d ** -0.5)
