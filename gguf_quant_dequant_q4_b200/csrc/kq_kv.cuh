@@ -129,6 +129,16 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The factor of a row's products q . k (q scaled by 2^e, the products by 2^-up)
+// to base-2 scores, kept among fp32's normal numbers.  Where it is cut the
+// softmax is the same: below, the scores are 0 to all bits; above, two products
+// that differ (by 2^-72 at least, the operands being binary16) are 2^55 apart.
+__device__ __forceinline__ float factor_of(float scale, int e, int up) {
+    if (scale == 0.f) return 1.f;   // (and q is 0)
+    const float f = fabsf(scale) * exp2_int(-e) * exp2_int(up);
+    return fminf(fmaxf(f, 1.17549435e-38f), 3.40282347e38f);
+}
+
 // The prompt kernel (kq_kv_prompt.cu) on tcgen05: head sizes that it covers,
 // its work space and its launch.
 bool kv_prompt_covers(int head_dim);

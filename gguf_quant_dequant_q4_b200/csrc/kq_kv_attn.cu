@@ -452,8 +452,7 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
                 }
             }
             if (t == 0) {
-                // 2^24 of the codes and 2^-e of the row, in two steps (e reaches 126)
-                yrow[r] = p.scale == 0.f ? 1.f : fmaxf(fabsf(p.scale) * 16777216.f * exp2_int(-e), 1.17549435e-38f);
+                yrow[r] = factor_of(p.scale, e, 24);   // (codes enter as 2^-24)
                 const int pos = s.pos0 + i;
                 hirow[r] = p.causal ? min(pos, s.len - 1) : s.len - 1;
                 lorow[r] = p.window > 0 ? pos - p.window + 1 : 0;

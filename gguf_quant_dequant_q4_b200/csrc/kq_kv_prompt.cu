@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                     const int e = xscale_exp(mx, 13);
                     // the scale's sign goes into q, so that c > 0; scale 0: q = 0
                     const float up = p.scale == 0.f ? 0.f : copysignf(exp2_int(e), p.scale);
-                    c = p.scale == 0.f ? 1.f : fmaxf(fabsf(p.scale) * exp2_int(-e), 1.17549435e-38f);
+                    c = factor_of(p.scale, e, 0);
                     const uint32_t dst = sb + C::kQ + half * C::kTileB + row * 128 + (NB == 4 ? side * C::kHalfB : 0);
 #pragma unroll
                     for (int b = 0; b < HB; ++b)

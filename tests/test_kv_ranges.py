@@ -136,3 +136,12 @@ STEEP = [[(70, 1), (300, 2)], [(200, 3), (33, 16)], [(400, 150), (90, 40)]]
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_large_scores(seqs, d, q):
     check_steep(steep(seqs, d, q, 128), d ** -0.5)
+
+
+@pytest.mark.parametrize("q,scale", [(1e37, 0.0), (1e38, 0.0), (-1e38, 0.0), (3e38, 1e-3), (1e37, -0.05), (1e-38, 1e38), (1e-30, 1e33)])
+@pytest.mark.parametrize("seqs", STEEP)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_factors_at_the_ends_of_fp32(seqs, d, q, scale):
+    # the scores are finite, while the power of two that brings q to
+    # binary16, or its product with the scale, is near fp32's ends
+    check_steep(steep(seqs, d, q, 4096), scale or d ** -0.5)
