@@ -15,12 +15,12 @@
 //                  bytes (low + 16 high), from which the low sums come off at
 //                  the end, as does 8 sum P d
 // q is scaled by a power of two per row (as every decode kernel of this
-// library), so only P and P * d are rounded, to binary16, each by at most
-// 2^-11 of its value: P is relative to a reference 5 below the row's maximum,
-// which moves only when the maximum is more than 13 above it, and d is divided by a power of two
-// near the largest |d| of the value rows seen so far, so that neither small P
-// nor tiny or huge values leave binary16's range.  Maximum, sum and all
-// accumulators are fp32.
+// library), so only P and P * d are rounded, to binary16.  P is relative to a
+// reference 5 below the row's maximum, which moves only when the maximum is more
+// than 13 above it; d is in units of a power of two near the tile's largest, and
+// scales 2^10 times smaller get a pass of their own.  So each rounding of a
+// weight is at most 2^-11 of it, or 2^-20 of the row's largest weight where that
+// is more.  Maximum, sum and all accumulators are fp32.
 //
 // Work is cut by keys, not by sequences: the tiles of 32 keys of all
 // (sequence, key head, 8 or 16 rows) segments form one list, and every CTA of
@@ -61,6 +61,11 @@ constexpr int kMinShare = kSegCost + 7;   // least units of a CTA's share: a til
 // maximum is more than 13 above it: P, 2^(score - reference), stays within 2^13,
 // P * d below 2^15.
 constexpr float kPBias = 5.f, kLazy = 8.f;
+// A tile's value scales are taken in units 2^ve near their largest: ve moves
+// when the largest is 2^2 and more times it, or below 2^-kDrop of it.  Scales
+// below 2^-kBelow of the unit get a pass of their own, so that binary16's last
+// step, 2^-24, is at most 2^-19 of the largest P (2^5 at least) times the scale.
+constexpr int kDrop = 3, kBelow = 10;
 
 // A sequence's share of the work.
 struct Seq {
@@ -155,6 +160,17 @@ __device__ __forceinline__ int list_find(const AttnParams& p, int64_t u, int64_t
 __device__ __forceinline__ int64_t share_of(int64_t total, int n_ctas) {
     const int64_t s = (total + n_ctas - 1) / n_ctas;
     return s < kMinShare ? kMinShare : s;
+}
+
+// Exponent of the value scale 2^ve that brings a binary16 magnitude to [1, 2)
+// (to 2^2 above 2^14, below 1 from subnormals).
+__device__ __forceinline__ int exponent_of(uint32_t mag) {
+    const int e = static_cast<int>(mag >> 10) - 15;
+    return e > 14 ? 14 : (e < -14 ? -14 : e);
+}
+// 2^e as binary16 bits; 0 below its smallest.
+__device__ __forceinline__ uint32_t bits_of_exp2(int e) {
+    return e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : (e >= -24 ? 1u << (e + 24) : 0u);
 }
 
 // x *= f in its own register (a rarely taken branch must not rename what the
@@ -607,9 +623,9 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
                                 l[nt][k & 1] = __int_as_float(0x7fc00000);
             }
             // ---- reference (kPBias below a maximum), value exponent
-            int ne = static_cast<int>(dmx >> 10) - 15;
-            ne = ne > 14 ? 14 : ne;
-            bool grow = ne > ve + 1;
+            int ne = exponent_of(dmx);
+            if (ne <= ve && (ne >= ve - kDrop || dmx == 0)) ne = ve;
+            bool grow = ne > ve + 1 || ne < ve;
             float mt[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -623,9 +639,8 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
                     grow |= v - m[nt][c] > kPBias + kLazy;   // (a difference of near values is exact)
                 }
             if (__any_sync(0xffffffffu, grow)) {
-                const int e = ne > ve ? ne : ve;
-                const float fe = exp2_int(ve - e);
-                ve = e;
+                const float fe = exp2_int(ve - ne);
+                ve = ne;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float f[2];
@@ -647,15 +662,6 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
                     for (int b = 0; b < NB; ++b) mul_in_place(pd[nt][b], (g & 1) ? fb : fa);
                 }
             }
-            {
-                const uint32_t vs = static_cast<uint32_t>((15 - ve) << 10) * 0x10001u;   // 2^-ve
-#pragma unroll
-                for (int b = 0; b < NB; b += 2) {
-                    const uint32_t two = hmul2_u32(dv[b] | (dv[b + 1] << 16), vs);
-                    sts_u16(scale_at + 64 * b, two);
-                    sts_u16(scale_at + 64 * b + 64, two >> 16);
-                }
-            }
             // ---- P (binary16), transposed into B operand words
             uint32_t pb[2][NT][2];
 #pragma unroll
@@ -675,34 +681,83 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
                     pb[j][nt][1] = movm(pack_f16x2(e[2], e[3]));
                 }
             }
-            // ---- O
-            __syncwarp();
-            uint4 dq[NB];   // scales of the keys 2t, 2t + 1, 2t + 8, 2t + 9 of both 16s
+            // ---- O, in passes over the scales' magnitudes: 2^ve times 2^-kBelow and
+            // more, then what is smaller in units of its own (rare)
+            uint32_t cut;
+#pragma unroll 1
+            for (;;) {
+                const uint32_t vs = static_cast<uint32_t>((15 - ve) << 10) * 0x10001u;   // 2^-ve
+                uint32_t two[NB / 2];
+                bool small = false;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) dq[b] = lds128(scales + 64 * b + 16 * t);
+                for (int b = 0; b < NB; b += 2) {
+                    two[b / 2] = hmul2_u32(dv[b] | (dv[b + 1] << 16), vs);
+                    small |= !__hbge2(__habs2(*reinterpret_cast<__half2*>(&two[b / 2])), __float2half2_rn(1.f / (1 << kBelow)));
+                }
+                uint32_t late = 0;   // the largest scale that is left for later
+                if (__any_sync(0xffffffffu, small)) {
+                    cut = bits_of_exp2(ve - kBelow);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t ra = vb + tau(j, 2 * t) * RB, rb = vb + tau(j, 2 * t + 1) * RB;
-                const uint32_t rc = vb + tau(j, 2 * t + 8) * RB, rd = vb + tau(j, 2 * t + 9) * RB;
+                    for (int b = 0; b < NB; ++b) {
+                        const uint32_t mag = dv[b] & 0x7fffu;
+                        if (mag < cut) {
+                            late = max(late, mag);
+                            two[b / 2] &= b & 1 ? 0xffffu : 0xffff0000u;
+                        }
+                    }
+                    late = __reduce_max_sync(0xffffffffu, late);
+                }
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const uint32_t c = 18 * b + 2 + 2 * g;
-                    const uint32_t xa = lds_u16(ra + c), xb = lds_u16(rb + c), xc = lds_u16(rc + c), xd = lds_u16(rd + c);
-                    // whole bytes (low code + 16 * high code) of both keys, and the low codes
-                    const uint32_t x0 = __byte_perm(xa, xb, 0x6420), x1 = __byte_perm(xa, xb, 0x6521);
-                    const uint32_t z0 = __byte_perm(xc, xd, 0x6420), z1 = __byte_perm(xc, xd, 0x6521);
-                    const uint32_t d0 = j ? dq[b].z : dq[b].x, d1 = j ? dq[b].w : dq[b].y;
+                for (int b = 0; b < NB; b += 2) {
+                    sts_u16(scale_at + 64 * b, two[b / 2]);
+                    sts_u16(scale_at + 64 * b + 64, two[b / 2] >> 16);
+                }
+                __syncwarp();
+                uint4 dq[NB];   // scales of the keys 2t, 2t + 1, 2t + 8, 2t + 9 of both 16s
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint32_t b0 = hmul2_u32(pb[j][nt][0], d0), b1 = hmul2_u32(pb[j][nt][1], d1);
-                        // rows g, g + 8: dims 2g, 2g + 1 of the block's first (then second) 16
-                        mma_f16(o[2 * b][nt], x0 & 0x000f000fu, x1 & 0x000f000fu, z0 & 0x000f000fu, z1 & 0x000f000fu, b0, b1);
-                        mma_f16(o[2 * b + 1][nt], x0, x1, z0, z1, b0, b1);
-                        pd[nt][b] = add_f16hi(b1, add_f16lo(b1, add_f16hi(b0, add_f16lo(b0, pd[nt][b]))));
+                for (int b = 0; b < NB; ++b) dq[b] = lds128(scales + 64 * b + 16 * t);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t ra = vb + tau(j, 2 * t) * RB, rb = vb + tau(j, 2 * t + 1) * RB;
+                    const uint32_t rc = vb + tau(j, 2 * t + 8) * RB, rd = vb + tau(j, 2 * t + 9) * RB;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const uint32_t c = 18 * b + 2 + 2 * g;
+                        const uint32_t xa = lds_u16(ra + c), xb = lds_u16(rb + c), xc = lds_u16(rc + c), xd = lds_u16(rd + c);
+                        // whole bytes (low code + 16 * high code) of both keys, and the low codes
+                        const uint32_t x0 = __byte_perm(xa, xb, 0x6420), x1 = __byte_perm(xa, xb, 0x6521);
+                        const uint32_t z0 = __byte_perm(xc, xd, 0x6420), z1 = __byte_perm(xc, xd, 0x6521);
+                        const uint32_t d0 = j ? dq[b].z : dq[b].x, d1 = j ? dq[b].w : dq[b].y;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint32_t b0 = hmul2_u32(pb[j][nt][0], d0), b1 = hmul2_u32(pb[j][nt][1], d1);
+                            // rows g, g + 8: dims 2g, 2g + 1 of the block's first (then second) 16
+                            mma_f16(o[2 * b][nt], x0 & 0x000f000fu, x1 & 0x000f000fu, z0 & 0x000f000fu, z1 & 0x000f000fu, b0, b1);
+                            mma_f16(o[2 * b + 1][nt], x0, x1, z0, z1, b0, b1);
+                            pd[nt][b] = add_f16hi(b1, add_f16lo(b1, add_f16hi(b0, add_f16lo(b0, pd[nt][b]))));
+                        }
                     }
                 }
+                __syncwarp();
+                if (late == 0) break;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {   // (P is 0 for what is not visible)
+                    dv[b] = lds_u16(vb + lane * RB + 18 * b);
+                    if ((dv[b] & 0x7fffu) >= cut) dv[b] = 0;
+                }
+                const int e = exponent_of(late);
+                const float f = exp2_int(ve - e);
+                ve = e;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int k = 0; k < 2 * NB; ++k)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) mul_in_place(o[k][nt][c], f);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) mul_in_place(pd[nt][b], f);
+                }
             }
-            __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
         }
 

@@ -145,3 +145,70 @@ def test_factors_at_the_ends_of_fp32(seqs, d, q, scale):
     # the scores are finite, while the power of two that brings q to
     # binary16, or its product with the scale, is near fp32's ends
     check_steep(steep(seqs, d, q, 4096), scale or d ** -0.5)
+
+
+# ---------------------------------------------- values of different magnitudes
+def rescale(case, b, j, factor, heads=slice(None), blocks=slice(None)):
+    """Multiplies the value scales of token j of sequence b by `factor`."""
+    raw = case.v[case.table[b, j // case.page], :, j % case.page].reshape(case.hkv, -1, 18)
+    d = np.ascontiguousarray(raw[..., :2]).view(np.float16)[..., 0]
+    d[heads, blocks] = (d[heads, blocks].astype(np.float64) * factor).astype(np.float16)
+    raw[..., :2] = d[..., None].view(np.uint8)
+    case.v[case.table[b, j // case.page], :, j % case.page] = raw.reshape(case.hkv, -1)
+
+
+SMALL = (-14.0, -12.0)     # exponents of the ordinary value scales
+
+
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+@pytest.mark.parametrize("seqs,rows", [([(43, 3)], 2), ([(500, 4), (70, 2)], 3), ([(300, 60)], 59)])
+def test_a_later_tokens_values_do_not_blur_earlier_rows(d, seqs, rows):
+    # the sequence's last token, which only the last row sees, has values 2^24
+    # times the others'
+    case = _kv.Case(seqs, 4, 2, d, 16, seed=24, v_exp=SMALL)
+    rescale(case, 0, seqs[0][0] - 1, 2.0 ** 24)
+    got = attend(case, 0.1)
+    check(case, got, 0.1, wide=True)
+    check(rows_of(case.expected(0.1), slice(0, rows)), got[:rows], 0.1, wide=True)
+
+
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+@pytest.mark.parametrize("where", [0, 20, 39])
+@pytest.mark.parametrize("new", [1, 3, 33])
+def test_large_values_of_no_weight(d, where, new):
+    # every query is positive and one key is far below zero: its weight is 0,
+    # its values 2^24 times the others'
+    case = _kv.Case([(40, new)], 4, 2, d, 16, seed=25, v_exp=SMALL)
+    case.q = case.q.abs()
+    case.k[case.table[0, where // 16], :, where % 16] = _kv.encode(np.full((2, d), -200.0, np.float32))
+    rescale(case, 0, where, 2.0 ** 24)
+    check(case, attend(case, 0.1), 0.1, wide=True)
+
+
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+@pytest.mark.parametrize("new", [1, 4, 60])
+@pytest.mark.parametrize("low", [-12, -16, -20, -24])
+def test_blocks_of_different_magnitudes(d, new, low):
+    # the first block's scales are 2^2 and more, the others' 2^low
+    case = _kv.Case([(300, new), (70, 1)], 4, 2, d, 16, seed=26, v_exp=(0.0, 1.0))
+    for b, (n, _) in enumerate(case.seqs):
+        for j in range(n):
+            rescale(case, b, j, 4.0, blocks=0)
+            rescale(case, b, j, 2.0 ** low, blocks=slice(1, None))
+    check(case, attend(case, 0.1), 0.1, wide=True)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 4, 60])
+@pytest.mark.parametrize("up", [False, True])
+def test_magnitudes_that_rise_or_fall(d, new, up):
+    # value scales from 2^12 to 2^-23 along the sequence (or back), and weights
+    # that move the other way, by 2^16
+    n, hq = 1200, 4
+    case = _kv.Case([(n, new)], hq, 2, d, 16, seed=27, v_exp=(0.0, 0.5))
+    exps = np.linspace(12, -23, n) if not up else np.linspace(-23, 12, n)
+    for j in range(n):
+        rescale(case, 0, j, 2.0 ** exps[j])
+        case.k[case.table[0, j // 16], :, j % 16] = _kv.encode(np.full((2, d), (-1 if up else 1) * (j - n / 2) / n * 16, np.float32))
+    case.q = torch.ones_like(case.q)
+    check(case, attend(case, np.log(2) / d), np.log(2) / d, wide=True)
