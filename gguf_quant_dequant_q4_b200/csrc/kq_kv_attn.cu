@@ -162,11 +162,11 @@ __device__ __forceinline__ int64_t share_of(int64_t total, int n_ctas) {
     return s < kMinShare ? kMinShare : s;
 }
 
-// Exponent of the value scale 2^ve that brings a binary16 magnitude to [1, 2)
-// (to 2^2 above 2^14, below 1 from subnormals).
+// Exponent of the value scale 2^ve that brings a binary16 magnitude (8188 at
+// most) to [1, 2), below 1 from subnormals.
 __device__ __forceinline__ int exponent_of(uint32_t mag) {
     const int e = static_cast<int>(mag >> 10) - 15;
-    return e > 14 ? 14 : (e < -14 ? -14 : e);
+    return e < -14 ? -14 : e;
 }
 // 2^e as binary16 bits; 0 below its smallest.
 __device__ __forceinline__ uint32_t bits_of_exp2(int e) {
@@ -593,35 +593,46 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
             }
             // ---- value scales, lane = key; a key that no row sees has 0
             uint32_t dv[NB];
-            uint32_t dm = 0;
+            uint32_t dm = 0, km = 0;   // largest of the key's value and key scales
             {
 #pragma unroll
                 for (int b = 0; b < NB; ++b) dv[b] = lds_u16(vb + lane * RB + 18 * b);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) km = max(km, lds_u16(kb + lane * RB + 18 * b) & 0x7fffu);
                 if (edge) {
                     const int key = key0 + lane;
                     const bool seen = key < s.len && key >= s.lo && ((there >> lane) & 1u);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) dv[b] = seen ? dv[b] : 0;
+                    km = seen ? km : 0;
                 }
 #pragma unroll
                 for (int b = 0; b < NB; ++b) dm = max(dm, dv[b] & 0x7fffu);
             }
-            const uint32_t dmx = __reduce_max_sync(0xffffffffu, dm);
-            if (dmx >= 0x7c00u) {
-                // a scale that is not finite: 0 in the product, and the rows that see its key become NaN
-                const unsigned who = __ballot_sync(0xffffffffu, dm >= 0x7c00u);
+            // a scale past 8188: the rows that see its key are not numbers (the
+            // prompt kernel's rule, whose binary16 values end there)
+            const unsigned who = __ballot_sync(0xffffffffu, max(dm, km) > 0x6fffu);
+            if (who) {
+                if ((who >> lane) & 1u) {
+                    dm = 0;
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    if ((dv[b] & 0x7c00u) == 0x7c00u) dv[b] = 0;
+                    for (int b = 0; b < NB; ++b) dv[b] = 0;
+                }
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (((who >> tau(j, g + 8 * (k >> 1))) & 1u) && y[j][nt][k] != -INFINITY)
-                                l[nt][k & 1] = __int_as_float(0x7fc00000);
+                        for (int k = 0; k < 4; ++k) {
+                            const int tk = tau(j, g + 8 * (k >> 1)), key = key0 + tk;
+                            const int r = nt * 8 + 2 * t + (k & 1);
+                            if ((who >> tk) & 1u) {
+                                if (key <= hirow[r] && key >= lorow[r]) l[nt][k & 1] = __int_as_float(0x7fc00000);
+                                y[j][nt][k] = -INFINITY;
+                            }
+                        }
             }
+            const uint32_t dmx = __reduce_max_sync(0xffffffffu, dm);
             // ---- reference (kPBias below a maximum), value exponent
             int ne = exponent_of(dmx);
             if (ne <= ve && (ne >= ve - kDrop || dmx == 0)) ne = ve;

@@ -455,12 +455,10 @@ int kq_kv_attention_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_
  * Query head h reads key head h / (n_heads / n_kv_heads).  Scores, softmax
  * statistics and outputs are accumulated in fp32; probabilities are rounded to
  * binary16.  Deterministic (no atomics on data).  A non-finite q sets
- * KQ_DEV_X_RANGE.  A cached key or value whose block scale is not finite makes
- * the rows that see it NaN (with few new tokens a key whose score comes out as
- * minus infinity has weight 0 instead; with many also rows that see keys on
- * both sides of it are NaN, and cached values past 65504 in magnitude, scales
- * past 8188, count as such).  n_tokens, window and max_blocks * page_size <= 2^30 -
- * 2^16, n_seqs <= 2^20, n_tokens * n_heads / n_kv_heads < 2^31 - 256.
+ * KQ_DEV_X_RANGE.  A cached key or value with a block scale past 8188 in
+ * magnitude (values past 65504) or not finite makes the rows that see it NaN.
+ * n_tokens, window and max_blocks * page_size <= 2^30 - 2^16, n_seqs <= 2^20,
+ * n_tokens * n_heads / n_kv_heads < 2^31 - 256.
  */
 int kq_kv_attention(int type, const uint16_t* q, int64_t n_tokens, int64_t q_stride, int32_t n_heads,
                     int32_t n_kv_heads, int32_t head_dim, const int32_t* cu_new, const int32_t* seq_lens,

@@ -212,3 +212,27 @@ def test_magnitudes_that_rise_or_fall(d, new, up):
         case.k[case.table[0, j // 16], :, j % 16] = _kv.encode(np.full((2, d), (-1 if up else 1) * (j - n / 2) / n * 16, np.float32))
     case.q = torch.ones_like(case.q)
     check(case, attend(case, np.log(2) / d), np.log(2) / d, wide=True)
+
+
+# --------------------------------------------------------- scales out of range
+@pytest.mark.parametrize("pool", ["k", "v"])
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+@pytest.mark.parametrize("word", [0x7e, 0x7c, 0xfc, 0x71, 0xf1])   # NaN, infinite of both signs, 10240 and more
+@pytest.mark.parametrize("new", [1, 6, 50])
+def test_scales_out_of_range(pool, d, word, new):
+    # the same rule for few rows and for prompts: rows that see the token are
+    # not numbers, whatever max_new chooses; the other rows are what they are
+    case = _kv.Case([(120, new), (90, 2)], 4, 2, d, 16, seed=28)
+    want = case.expected(0.1, True, 4)
+    at = max(120 - new - 2, 120 - 30)              # the rows at positions at .. at + 3 see it
+    raw = case.k if pool == "k" else case.v
+    raw[case.table[0, at // 16], 1, at % 16, 19] = word      # the second block's scale of head 1
+    see = np.zeros((new + 2, 4), bool)
+    see[:new, 2:] = ((np.arange(120 - new, 120) >= at) & (np.arange(120 - new, 120) < at + 4))[:, None]
+    fine = torch.from_numpy(~see)
+    for most in (case.max_new, 2000):
+        case.max_new = most
+        got = attend(case, 0.1, True, 4).cpu()
+        assert torch.isnan(got[~fine]).all() and see.any()
+        part = rows_of(want, see == False)         # noqa: E712
+        check(part, got[fine], 0.1, wide=True)
