@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
     static_assert(sizeof(Bars) <= 512, "barriers");
     volatile uint32_t* tmask = reinterpret_cast<volatile uint32_t*>(smem + 512);  // [16] runs of a tile that are there
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + 576);   // tensor memory, abort
-    // [8] segments in turn: first and last key whose value scale is not finite
+    // [8] segments in turn: first and last key with a scale past 8188
     int* bad_lo = reinterpret_cast<int*>(smem + 640);
     int* bad_hi = bad_lo + 8;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -881,8 +881,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                 l += other(l);
                 if (__all_sync(0xffffffffu, wait(&bar.o_full[2 * half + 1], (hn + tiles - 1) & 1))) {
                     tc_fence_after();
-                    // a row that sees a key whose value scale is not finite
-                    if (bad_hi[seg & 7] >= lo && bad_lo[seg & 7] <= hi && there) l = __int_as_float(0x7fc00000);
+                    // a row that sees a key with a scale past 8188
+                    const int b0 = bad_lo[seg & 7], b1 = bad_hi[seg & 7];
+                    bool bad = there && b1 >= lo && b0 <= hi;
+                    if (bad && b0 < lo && b1 > hi) {
+                        // one before and one behind the row's keys: look at its own
+                        bad = false;
+                        const int end = min(hi, (sp.t0 + pt.t0 + tiles) * kKeys - 1);
+#pragma unroll 1
+                        for (int key = max(lo, (sp.t0 + pt.t0) * kKeys); key <= end && !bad; ++key) {
+                            const int blk = page_of(p, key), pg = p.table[static_cast<int64_t>(at.b) * p.max_blocks + blk];
+                            if (pg < 0 || pg >= p.n_pages) continue;
+                            const int64_t off = ((static_cast<int64_t>(pg) * p.n_kv + at.h) * p.page + (key - blk * p.page)) * RB;
+#pragma unroll 1
+                            for (int b = 0; b < NB; ++b) {
+                                const int kd = *reinterpret_cast<const uint16_t*>(p.kp + off + 18 * b) & 0x7fff;
+                                const int vd = *reinterpret_cast<const uint16_t*>(p.vp + off + 18 * b) & 0x7fff;
+                                bad |= max(kd, vd) > 0x6fff;
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    if (bad) l = __int_as_float(0x7fc00000);
                     const float inv = l == 0.f ? 0.f : 1.f / l;
                     float* part = parts_of(p) + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * C::kSlot;
                     uint16_t* out = p.out + (static_cast<int64_t>(s.tok0 + ti) * p.n_heads + qhead) * D + D / 2 * side;

@@ -236,3 +236,22 @@ def test_scales_out_of_range(pool, d, word, new):
         assert torch.isnan(got[~fine]).all() and see.any()
         part = rows_of(want, see == False)         # noqa: E712
         check(part, got[fine], 0.1, wide=True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window", [10, 30])
+def test_rows_between_two_scales_out_of_range(d, window):
+    # a window that holds neither of the two tokens: the rows between are numbers
+    case = _kv.Case([(400, 400), (700, 65)], 2, 1, d, 16, seed=29)
+    want = case.expected(0.1, True, window)
+    case.k[case.table[0, 130 // 16], 0, 130 % 16, 1] = 0x7e
+    case.v[case.table[0, 240 // 16], 0, 240 % 16, 19] = 0x7c
+    case.v[case.table[1, 636 // 16], 0, 636 % 16, 19] = 0x7c
+    got = attend(case, 0.1, True, window)
+    pos = np.concatenate([np.arange(400), 635 + np.arange(65)])
+    first = np.arange(465) < 400
+    see = np.where(first, ((pos >= 130) & (pos < 130 + window)) | ((pos >= 240) & (pos < 240 + window)),
+                   (pos >= 636) & (pos < 636 + window))
+    assert torch.isnan(got[torch.from_numpy(see).cuda()]).all()
+    fine = np.flatnonzero(~see)
+    check(rows_of(want, fine), got[torch.from_numpy(fine).cuda()], 0.1, wide=True)
