@@ -370,6 +370,7 @@ struct Bars {
     uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t s_full[4], p_full[4], o_full[4], q_full[2];   // [2 half + side]
     uint64_t m_full[16];                                   // [softmax warp]
+    uint64_t idle;                                         // second half: a segment without its rows has begun
 };
 
 template <int NB>
@@ -407,6 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
             mbar_init(&bar.o_full[i], 1);
         }
         for (int i = 0; i < 16; ++i) mbar_init(&bar.m_full[i], 1);
+        mbar_init(&bar.idle, 1);
         for (int i = 0; i < 8; ++i) {
             bad_lo[i] = 0x7fffffff;
             bad_hi[i] = -1;
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
             const uint64_t qd = sw128_desc(sb + C::kQ + i * C::kTileB, 16), kd = sw128_desc(sb + C::kK, 16),
                            vd = sw128_desc(sb + C::kV, C::kHalfB);
             uint32_t n = 0;           // tiles so far
-            uint32_t hn = 0, hs = 0;  // tiles and segments of this half (the second may be idle)
+            uint32_t hn = 0, hs = 0;  // tiles of this half (the second may be idle), segments
             bool ok = true;
             auto await = [&](uint64_t* b, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && wait(b, parity)); };
             auto qk = [&](int z, uint32_t m) {   // S of side z = q K^T, tile number m
@@ -464,11 +466,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                 const Part pt = part_of(at, span_of(p, s, at.rt), left);
                 const int tiles = __shfl_sync(0xffffffffu, pt.n, 0);
                 const bool used = __shfl_sync(0xffffffffu, tiles > 0 && (i == 0 || s.rows - at.rt * kRows > 128), 0);
-                if (used) {
+                if (tiles > 0) {
+                    // (an idle half's softmax warps are waited for all the same, so that
+                    // they have read the notes on the segment before)
                     await(&bar.q_full[i], hs & 1);
                     ++hs;
-                }
-                if (tiles > 0) {
+                    if (ok && !used && elect_one()) mbar_arrive(&bar.idle);
+                    __syncwarp();
                     await(&bar.k_full[n & 1], (n >> 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
@@ -685,6 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
         };
         uint32_t n = 0;                // tiles so far
         uint32_t hn = 0, seg = 0;      // tiles of this half, segments
+        uint32_t idle = 0;             // segments without rows of this half
         int slot = 0;
         for (; left > 0;) {
             const Span sp = span_of(p, s, at.rt);
@@ -948,8 +953,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const AttnParams p)
                     }
                 }
                 hn += tiles;
+            } else if (tiles > 0) {
+                // this half has no rows here, but keeps in step with its issuer
+                if (lane == 0) mbar_arrive(&bar.q_full[half]);
+                wait(&bar.idle, idle & 1);
+                ++idle;
             }
-            // the slot of the segment four on is long read, and not yet written
+            // the slot of the segment four on: the halves are at most two tiles
+            // apart, the decoders at most two tiles ahead of the slower one
             if (tiles > 0 && tid == 0) {
                 bad_lo[(seg + 4) & 7] = 0x7fffffff;
                 bad_hi[(seg + 4) & 7] = -1;

@@ -255,3 +255,24 @@ def test_rows_between_two_scales_out_of_range(d, window):
     assert torch.isnan(got[torch.from_numpy(see).cuda()]).all()
     fine = np.flatnonzero(~see)
     check(rows_of(want, fine), got[torch.from_numpy(fine).cuda()], 0.1, wide=True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_prompts_beside_scales_out_of_range(d):
+    # several short prompts a CTA, some of more than 128 rows a key head; every
+    # fifth sequence has a value whose scale is not a number
+    rng = np.random.default_rng(d)
+    seqs = [(int(n) + 40, int(min(n, m))) for n, m in zip(rng.integers(34, 160, 70), rng.integers(34, 160, 70))]
+    case = _kv.Case(seqs, 16, 8, d, 16, seed=30)
+    want = case.expected(0.1, True, 40)
+    bad = np.zeros((len(case.q), 16), bool)
+    for b in range(0, len(seqs), 5):
+        n, m = seqs[b]
+        at, h = n - m // 2, b % 8
+        case.v[case.table[b, at // 16], h, at % 16, 1] = 0x7e
+        pos = n - m + np.arange(m)
+        bad[case.cu[b]:case.cu[b + 1], 2 * h:2 * h + 2] = ((pos >= at) & (pos < at + 40))[:, None]
+    for _ in range(3):
+        got = attend(case, 0.1, True, 40).cpu()
+        assert torch.isnan(got[torch.from_numpy(bad)]).all()
+        check(rows_of(want, ~bad), got[torch.from_numpy(~bad)], 0.1, wide=True)
