@@ -525,7 +525,10 @@ def kv_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, qt
     cached keys and values of their sequences, bfloat16 of q's shape.  seq_lens,
     cu_new as kv_plan gives them; max_new: the largest number of new tokens of a
     sequence; scale defaults to head_dim ** -0.5; window 0: no window.  A token
-    that sees no key gets zeros; rows of no sequence are left as they are."""
+    that sees no key gets zeros; rows of no sequence are left as they are.  A
+    sequence longer than its table row keeps its positions, what is past the row
+    is hidden and err gets DEV_TOO_MANY.  A block scale past 8188 or not finite
+    makes the rows that see it NaN."""
     q = _bf16_bits(q)
     qs = _token_rows(q, "q")
     t, hq, d = q.shape

@@ -33,15 +33,18 @@
 // results in the work space, joined in list order by a second kernel: no
 // atomics on data, the same result on every run.
 //
-// Bound by instruction issue, close to HBM (0.5625 bytes a cached value):
-// one sequence of 700 keys, 32 heads over 8 of 128: 13.9 us; 24 of up to 4100
-// keys, 16 over 16 of 64: 31.5; 16 of up to 6000 with 3 to 5 tokens each and a
-// window, 16 over 4 of 256: 35.4; 48 of up to 8192, 32 over 8 of 128: 67 us
-// (3.3 TB/s); 2 of 150,000 to 200,000, 64 over 8 of 128: 95.6 us (4.2 TB/s).
+// Bound by latency at the few warps that the registers leave (3.7 a scheduler:
+// 57 % of the issue slots, 48 % of the ALU pipe, 44 % of DRAM's peak), and with
+// short segments by their starts and joins.  Kernels alone: one sequence of 700
+// keys, 32 heads over 8 of 128: 13.9 us; 24 of up to 4100 keys, 16 over 16 of
+// 64: 33; 16 of up to 6000 with 3 to 5 tokens each and a window, 16 over 4 of
+// 256: 39; 48 of up to 8192, 32 over 8 of 128: 69 (3.3 TB/s); 2 of 150,000 to
+// 200,000, 64 over 8 of 128: 98 (4.1 TB/s; 103 after seconds at the power cap).
 // What the steps were worth on the last of these: work split by keys 143 us;
 // four producer lanes a tile, value scales through a table 117; q in shared
 // memory, in-place rescaling, whole bytes 100; segments' fixed cost in the
-// split 96 (and 87 -> 67 on the ragged batch).  Fetching by the consumer warps
+// split 96 (and 87 -> 67 on the ragged batch); scores and value scales of any
+// size 98 (and 69).  Fetching by the consumer warps
 // themselves instead of a producer: 115, more warps at fewer registers: 117 to
 // 133, -8 by exact subtraction from every operand: 117.
 #include "kq_kv.cuh"
@@ -53,8 +56,9 @@ constexpr int kTile = 32;        // keys of a tile
 // A segment counts as its tiles and kSegCost more in the list: its queries,
 // first copies and join take about as long as that many tiles.  A CTA whose
 // part of a segment is within these has nothing to do there.  (Ragged batch of
-// 48 sequences up to 8192 keys: 87 us without, 70 with 12, 68 with 20, 70 with
-// 28, 78 with 60.)
+// 48 sequences up to 8192 keys, heads of 128: 87 us without, 70 with 12, 68 with
+// 20, 70 with 28, 78 with 60; chosen on this batch, the other shapes take the
+// same.)
 constexpr int kSegCost = 20;
 constexpr int kMinShare = kSegCost + 7;   // least units of a CTA's share: a tile a warp
 // A row's reference is 5 below its maximum when it moves, which it does when the

@@ -38,16 +38,19 @@
 //
 // Bound by the chain of waits of a side (S, softmax, P, its MMAs); neither the
 // tensor pipe nor the exponentials (each about half of the time) are full:
-// the last 2048 tokens of 8048, 32 heads over 8 of 128: 255 us (0.92 PFLOP/s);
+// the last 2048 tokens of 8048, 32 heads over 8 of 128: 262 us (0.90 PFLOP/s;
+// 284 after a second or so, when the power cap takes the clock to 1.8 GHz);
 // ragged prompts of up to 2500 tokens and as many as 1500 keys before them, 24
-// heads over 8 of 64: 290 us (0.45 PFLOP/s).
+// heads over 8 of 64: 290 us (0.45 PFLOP/s), where the exponentials of the
+// visible scores alone are 109 us.  Registers are short: 60 bytes of a thread are
+// spilled with 128-value heads, 264 with 64.
 // What the steps were worth on the first of these: 16-row mma.sync tiles 2513
 // us; this kernel with one softmax thread a row 402; two threads a row and the
 // plan by one CTA 306; MMAs issued by an elected lane of a whole warp 286; S by
-// 32 keys, without spills, 278; 64 keys a side and one issuing warp 335, with
-// two 279; the reference handed over in one look 267; handed on half way and
-// fewer polls 255.  A cubic on the FMA pipe for 1/4 of the exponentials: 288
-// for 266; a side's 64 keys in registers at once: 292 for 266; Q K^T of both
+// 32 keys 278; 64 keys a side and one issuing warp 335, with two 279; the
+// reference handed over in one look 267; handed on half way and fewer polls 255;
+// scores of any size and out-of-range keys by row 262.  A cubic on the FMA pipe
+// for 1/4 of the exponentials: 288 for 266; a side's 64 keys in registers at once: 292 for 266; Q K^T of both
 // sides at once: 340 for 279 (64 keys cost 51 cycles an MMA, 128 67, but the
 // sides wait for each other); polls without a pause: 302 for 266; P beside S
 // with 64-value heads, the next Q K^T under the softmax: ragged 309 for 290.
@@ -62,7 +65,8 @@ constexpr int kMmaWarp = kSoft + kDec, kLoadWarp = kMmaWarp + 2;
 constexpr int kThreads = 32 * (kSoft + kDec + 4);   // seven warpgroups (one warp idle)
 // A segment counts as its tiles and kSegCost more in the list: its queries,
 // first tiles and output take about as long as that many tiles (ragged prompts:
-// 304 us with 3, 290 with 4 or 5, 293 with 6).
+// 304 us with 3, 290 with 4 or 5, 293 with 6; chosen on these 64-value heads,
+// 128 take the same).
 constexpr int kSegCost = 4;
 constexpr int kRaw = 3;            // raw tiles in flight
 constexpr int kMinShare = kSegCost + 3;   // least units of a CTA's share

@@ -95,7 +95,8 @@ typedef enum {
 #define KQ_DEV_UNSORTED     0x8   /* expert ids not ascending                  */
 #define KQ_DEV_TIMEOUT      0x10  /* a bounded pipeline wait ran out            */
 #define KQ_DEV_TOO_MANY     0x20  /* KV cache: tokens past a limit of the call  */
-#define KQ_DEV_X_RANGE      0x40  /* an activation is infinite or NaN         */
+#define KQ_DEV_X_RANGE      0x40  /* an activation is infinite or NaN (or, on
+                                     kq_kv_append, past 65504)                */
 
 /* Block geometry of a codec (host only).  Returns KQ_OK or
  * KQ_ERR_UNSUPPORTED.  Source: mlx-kquant README, "Codec reference" table. */
@@ -453,8 +454,11 @@ int kq_kv_attention_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_
  *               calls that may run at the same time need one each.  Nothing
  *               in it has to be kept or cleared between calls.
  * Query head h reads key head h / (n_heads / n_kv_heads).  Scores, softmax
- * statistics and outputs are accumulated in fp32; probabilities are rounded to
- * binary16.  Deterministic (no atomics on data).  A non-finite q sets
+ * statistics and outputs are accumulated in fp32.  Rounded to binary16 are q
+ * (after a power of two for each row), the probabilities, and with few new
+ * tokens their products with the value scales (a probability is off by at most
+ * 2^-10 of itself or 2^-19 of the row's largest), with many the decoded keys and
+ * values.  Deterministic (no atomics on data).  A non-finite q sets
  * KQ_DEV_X_RANGE.  A cached key or value with a block scale past 8188 in
  * magnitude (values past 65504) or not finite makes the rows that see it NaN.
  * n_tokens, window and max_blocks * page_size <= 2^30 - 2^16, n_seqs <= 2^20,
