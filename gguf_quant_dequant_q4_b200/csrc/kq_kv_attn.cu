@@ -18,9 +18,9 @@
 // library), so only P and P * d are rounded, to binary16.  P is relative to a
 // reference 5 below the row's maximum, which moves only when the maximum is more
 // than 13 above it; d is in units of a power of two near the tile's largest, and
-// scales 2^10 times smaller get a pass of their own.  So each rounding of a
-// weight is at most 2^-11 of it, or 2^-20 of the row's largest weight where that
-// is more.  Maximum, sum and all accumulators are fp32.
+// scales 2^10 times smaller get a pass of their own.  So P is off by at most
+// 2^-11 of itself or 2^-30 of the row's largest weight, and P * d by 2^-11 of
+// itself or 2^-20 of the largest weight times d.  Maximum, sum and all accumulators are fp32.
 //
 // Work is cut by keys, not by sequences: the tiles of 32 keys of all
 // (sequence, key head, 8 or 16 rows) segments form one list, and every CTA of

@@ -7,7 +7,8 @@
 // accumulate in fp32 in tensor memory, P = 2^(y - m) goes back to tensor
 // memory as binary16 and is the second product's A operand.  The reference m,
 // 7 below the running maximum, is only moved when a row's new maximum is more
-// than 15 above it, so O is rescaled rarely; P stays below 2^15.1.
+// than 15 above it, so O is rescaled rarely; P stays below 2^15.1, and weights
+// below 2^-32 of the row's largest round to 0.
 //
 // Warp-specialized, one CTA an SM, 28 warps (one idle):
 //   warps 0..15   softmax, two threads a row: warps 0..7 rows 0..127 (first

@@ -455,10 +455,11 @@ int kq_kv_attention_workspace(int32_t n_heads, int32_t n_kv_heads, int32_t head_
  *               in it has to be kept or cleared between calls.
  * Query head h reads key head h / (n_heads / n_kv_heads).  Scores, softmax
  * statistics and outputs are accumulated in fp32.  Rounded to binary16 are q
- * (after a power of two for each row), the probabilities, and with few new
- * tokens their products with the value scales (a probability is off by at most
- * 2^-10 of itself or 2^-19 of the row's largest), with many the decoded keys and
- * values.  Deterministic (no atomics on data).  A non-finite q sets
+ * (after a power of two for each row), the probabilities (off by at most 2^-11
+ * of themselves or 2^-30 of the row's largest: what is below that counts as 0,
+ * however large its values), and with few new tokens their products with the
+ * value scales (2^-11 again, or 2^-20 of the largest probability times the
+ * scale), with many the decoded keys and values.  Deterministic (no atomics on data).  A non-finite q sets
  * KQ_DEV_X_RANGE.  A cached key or value with a block scale past 8188 in
  * magnitude (values past 65504) or not finite makes the rows that see it NaN.
  * n_tokens, window and max_blocks * page_size <= 2^30 - 2^16, n_seqs <= 2^20,

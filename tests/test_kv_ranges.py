@@ -40,6 +40,21 @@ def test_lengths_past_the_table_row(d, new, causal, window):
     assert int(err) == 0
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 7, 90])
+def test_the_longest_length(d, new):
+    # positions at the end of 32 bits: every key of the row is visible, none with a window
+    case = _kv.Case([(128, new), (50, 1)], 4, 2, d, 16, seed=31, spare=0)
+    want = case.expected(0.1, False)
+    case.lens[0] = 2 ** 31 - 1
+    err = flag()
+    check(rows_of(want, slice(None)), attend(case, 0.1, err=err), 0.1, wide=True)
+    assert int(err) == kq.DEV_TOO_MANY
+    got = attend(case, 0.1, True, 50)
+    assert bool((got[:new] == 0).all())
+    check(rows_of(want, slice(new, None)), got[new:], 0.1, wide=True)
+
+
 @pytest.mark.parametrize("d", [64, 192])
 @pytest.mark.parametrize("new", [10, 100])
 def test_offsets_past_the_tokens(d, new):
