@@ -755,10 +755,13 @@ __global__ void __launch_bounds__(Shape<NB, NT>::kThreads, Shape<NB, NT>::two ? 
                 }
                 __syncwarp();
                 if (late == 0) break;
+                // (what no row sees may be larger than `late`, and must not overflow)
+                const int key = key0 + lane;
+                const bool seen = key < s.len && key >= s.lo && ((there & ~who) >> lane) & 1u;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {   // (P is 0 for what is not visible)
+                for (int b = 0; b < NB; ++b) {
                     dv[b] = lds_u16(vb + lane * RB + 18 * b);
-                    if ((dv[b] & 0x7fffu) >= cut) dv[b] = 0;
+                    if (!seen || (dv[b] & 0x7fffu) >= cut) dv[b] = 0;
                 }
                 const int e = exponent_of(late);
                 const float f = exp2_int(ve - e);

@@ -229,6 +229,21 @@ def test_magnitudes_that_rise_or_fall(d, new, up):
     check(case, attend(case, np.log(2) / d), np.log(2) / d, wide=True)
 
 
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+@pytest.mark.parametrize("fill", [0x3fff, 0x43ff, 0x6fff, 0x0001])
+def test_leftovers_in_the_last_page(d, fill):
+    # behind the last token lie blocks with finite scales, beside visible ones
+    # from 2^12 down to 2^-24
+    case = _kv.Case([(37, 2), (70, 3), (5, 1)], 4, 2, d, 16, seed=32, v_exp=(-24.0, 12.0))
+    for pool in (case.k, case.v):
+        raw = pool.reshape(*pool.shape[:3], -1, 18)
+        raw[(raw == 255).all(-1)] = np.frombuffer(np.uint16(fill).tobytes() + bytes([0x1f] * 16), np.uint8)
+    for window in (0, 30):
+        got = attend(case, 0.02, True, window)
+        assert torch.isfinite(got).all()
+        check(case, got, 0.02, True, window, wide=True)
+
+
 # --------------------------------------------------------- scales out of range
 @pytest.mark.parametrize("pool", ["k", "v"])
 @pytest.mark.parametrize("d", [64, 128, 192, 256])
